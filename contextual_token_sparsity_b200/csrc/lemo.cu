@@ -12,14 +12,17 @@
 
 #include "lemo.h"
 #include "attn.cuh"
+#include "ckpt.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
 #include "mlp.cuh"
 #include "move.cuh"
+#include "norm.cuh"
 #include "predict.cuh"
 #include "score.cuh"
 #include "segloss.cuh"
 #include "select.cuh"
+#include "wgrad.cuh"
 
 namespace {
 
@@ -1104,6 +1107,454 @@ lemo_status lemo_segment_loss(const uint16_t* h, int64_t ld_h, int64_t T, int32_
         }
     }
     launch(sl::loss_kernel, 1, sl::kCountThreads, 0, st, tl, T, n_valid, loss);
+    return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- norms around a sublayer, 8-bit checkpoints -----------------------------
+
+bool mat_ok(const void* p, int64_t ld, int64_t width) {
+    return p && aligned(p, 16) && ld >= width && ld % 8 == 0;
+}
+bool vec_ok(const void* p) { return !p || aligned(p, 16); }
+bool f32_ok(const void* p) { return !p || aligned(p, 4); }
+
+lemo_status check_rows(int64_t rows, int32_t d, const int32_t* kept_idx,
+                       const int32_t* kept_total) {
+    if (d < 1 || rows < 0 || rows > INT_MAX) return LEMO_ERR_INVALID_ARG;
+    if (d % 8 != 0) return LEMO_ERR_UNSUPPORTED;
+    if (!kept_total || !aligned(kept_total, 4) || !aligned(kept_idx, 4)) return LEMO_ERR_INVALID_ARG;
+    return LEMO_OK;
+}
+
+lemo_status check_checkpoint(const lemo_checkpoint* c, int32_t d, int64_t rows) {
+    if (!c || !c->data || !c->scales) return LEMO_ERR_INVALID_ARG;
+    if (c->format != LEMO_CHECKPOINT_E4M3 && c->format != LEMO_CHECKPOINT_INT8)
+        return LEMO_ERR_INVALID_ARG;
+    if (c->d != d || c->rows < rows) return LEMO_ERR_INVALID_ARG;
+    if (!aligned(c->data, 16) || c->ld_data % 16 != 0 || c->ld_data < d) return LEMO_ERR_INVALID_ARG;
+    if (!aligned(c->scales, 4) || c->ld_scales % 4 != 0 ||
+        c->ld_scales < (d + lemo::ckpt::kGroup - 1) / lemo::ckpt::kGroup)
+        return LEMO_ERR_INVALID_ARG;
+    return LEMO_OK;
+}
+
+lemo::ckpt::View view_of(const lemo_checkpoint* c) {
+    lemo::ckpt::View v = {};
+    v.format = lemo::ckpt::kNone;
+    if (c) {
+        v.format = c->format;
+        v.data = c->data;
+        v.ld = c->ld_data;
+        v.scales = c->scales;
+        v.ld_scales = c->ld_scales;
+    }
+    return v;
+}
+
+const uint4* vecs(const uint16_t* p) { return reinterpret_cast<const uint4*>(p); }
+uint4* vecs(uint16_t* p) { return reinterpret_cast<uint4*>(p); }
+
+// The group shape of a row of dvec 16-byte vectors: the fewest threads times
+// vectors that hold it.
+template <bool BWD, bool POST, int G, int V>
+void launch_norm(const lemo::norm::Args& a, int sms, cudaStream_t st, int* grid_out) {
+    namespace nm = lemo::norm;
+    constexpr int threads = nm::Shape<G, V>::kThreads;
+    int64_t grid = a.rows < 1 ? 1 : a.rows;
+    if (BWD) {
+        if (grid > nm::kMaxParts) grid = nm::kMaxParts;
+        if (grid > 2 * sms) grid = 2 * sms;
+        launch(nm::backward_kernel<G, V, POST>, (unsigned)grid, threads, 0, st, a);
+    } else {
+        if (grid > 4 * sms) grid = 4 * sms;
+        launch(nm::forward_kernel<G, V, POST>, (unsigned)grid, threads, 0, st, a);
+    }
+    *grid_out = (int)grid;
+}
+
+template <bool BWD, bool POST>
+lemo_status run_norm(const lemo::norm::Args& a, cudaStream_t st, int* grid) {
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms <= 0) return LEMO_ERR_CUDA;
+    if (a.dvec <= 32) launch_norm<BWD, POST, 32, 1>(a, sms, st, grid);
+    else if (a.dvec <= 64) launch_norm<BWD, POST, 32, 2>(a, sms, st, grid);
+    else if (a.dvec <= 128) launch_norm<BWD, POST, 64, 2>(a, sms, st, grid);
+    else if (a.dvec <= 256) launch_norm<BWD, POST, 128, 2>(a, sms, st, grid);
+    else if (a.dvec <= 512) launch_norm<BWD, POST, 256, 2>(a, sms, st, grid);
+    else if (a.dvec <= 768) launch_norm<BWD, POST, 256, 3>(a, sms, st, grid);
+    else if (a.dvec <= 1024) launch_norm<BWD, POST, 512, 2>(a, sms, st, grid);
+    else launch_norm<BWD, POST, 512, 4>(a, sms, st, grid);
+    return launch_status();
+}
+
+lemo_status run_column_sums(const lemo::norm::Args& n, int parts, const uint16_t* w,
+                            const uint16_t* b, const uint16_t* gate, float* dw, float* db,
+                            float* dgate, cudaStream_t st) {
+    namespace nm = lemo::norm;
+    nm::SumArgs s;
+    s.part = n.part;
+    s.d = n.d;
+    s.max_parts = parts;
+    s.kept_total = n.kept_total;
+    s.rows = n.rows;
+    s.w = w;
+    s.b = b;
+    s.gate = gate;
+    s.dw = dw;
+    s.db = db;
+    s.dgate = dgate;
+    launch(nm::column_sums_kernel, (unsigned)((n.d + nm::kSumCols - 1) / nm::kSumCols),
+           nm::kSumCols * nm::kSumSlices, 0, st, s);
+    return launch_status();
+}
+
+lemo::norm::Args norm_args(lemo_norm norm, int32_t d, const uint16_t* w, const uint16_t* b,
+                           const int32_t* kept_idx, const int32_t* kept_total, int64_t rows) {
+    lemo::norm::Args a = {};
+    a.kind = norm;
+    a.d = d;
+    a.dvec = d / 8;
+    a.inv_d = 1.f / (float)d;
+    a.w = vecs(w);
+    a.b = vecs(b);
+    a.kept_idx = kept_idx;
+    a.kept_total = kept_total;
+    a.rows = rows;
+    a.pad_to = 1;
+    a.scale = 1.f;
+    a.c.format = lemo::ckpt::kNone;
+    return a;
+}
+
+bool eps_ok(float eps) { return eps >= 0.f && eps < __builtin_inff(); }
+
+// Persistent grid of the element-wise checkpoint kernels.
+template <typename Kernel>
+int ckpt_grid(Kernel, int sms, int64_t warps) {
+    const int64_t per = lemo::ckpt::kThreads / 32;
+    int64_t grid = (warps + per - 1) / per;
+    if (grid < 1) grid = 1;
+    const int64_t most = (int64_t)sms * 8;
+    return (int)(grid < most ? grid : most);
+}
+
+}  // namespace
+
+extern "C" {
+
+lemo_status lemo_norm_gather(lemo_norm norm, const uint16_t* x, int64_t ld_x, int64_t x_rows,
+                             int32_t d, const uint16_t* weight, const uint16_t* bias, float eps,
+                             const int32_t* kept_idx, const int32_t* kept_total, int32_t pad_to,
+                             uint16_t* y, int64_t ld_y, int64_t rows, float* stats,
+                             const lemo_checkpoint* checkpoint, lemo_stream stream) {
+    lemo_status e = check_rows(rows, d, kept_idx, kept_total);
+    if (e != LEMO_OK) return e;
+    if (norm != LEMO_NORM_RMS && norm != LEMO_NORM_LAYER) return LEMO_ERR_INVALID_ARG;
+    if (d > lemo::norm::kMaxD) return LEMO_ERR_UNSUPPORTED;
+    if (!mat_ok(x, ld_x, d) || !mat_ok(y, ld_y, d) || x_rows < 0 || pad_to < 1 || !eps_ok(eps))
+        return LEMO_ERR_INVALID_ARG;
+    if (!vec_ok(weight) || !vec_ok(bias) || !aligned(stats, 8)) return LEMO_ERR_INVALID_ARG;
+    if (checkpoint && (e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
+    lemo::norm::Args a = norm_args(norm, d, weight, bias, kept_idx, kept_total, rows);
+    a.eps = eps;
+    a.x = vecs(const_cast<uint16_t*>(x));
+    a.ld_x = ld_x / 8;
+    a.x_rows = x_rows;
+    a.y = vecs(y);
+    a.ld_y = ld_y / 8;
+    a.stats = reinterpret_cast<float2*>(stats);
+    a.pad_to = pad_to;
+    a.c = view_of(checkpoint);
+    int grid = 0;
+    return run_norm<false, false>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
+}
+
+size_t lemo_norm_workspace_size(int32_t d) {
+    if (d < 1 || d % 8 != 0 || d > lemo::norm::kMaxD) return 0;
+    return lemo::align_up((size_t)lemo::norm::kMaxParts * 2 * (size_t)d * sizeof(float), 256);
+}
+
+lemo_status lemo_norm_gather_backward(lemo_norm norm, const uint16_t* dy, int64_t ld_dy,
+                                      int64_t rows, int32_t d, const uint16_t* weight,
+                                      const float* stats, const int32_t* kept_idx,
+                                      const int32_t* kept_total, const uint16_t* x, int64_t ld_x,
+                                      int64_t x_rows, const lemo_checkpoint* checkpoint,
+                                      uint16_t* dx, int64_t ld_dx, int64_t dx_rows,
+                                      float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                                      lemo_stream stream) {
+    lemo_status e = check_rows(rows, d, kept_idx, kept_total);
+    if (e != LEMO_OK) return e;
+    if (norm != LEMO_NORM_RMS && norm != LEMO_NORM_LAYER) return LEMO_ERR_INVALID_ARG;
+    if (d > lemo::norm::kMaxD) return LEMO_ERR_UNSUPPORTED;
+    if (!mat_ok(dy, ld_dy, d) || !mat_ok(dx, ld_dx, d) || dx_rows < 0) return LEMO_ERR_INVALID_ARG;
+    if (!stats || !aligned(stats, 8) || !vec_ok(weight) || !f32_ok(dweight) || !f32_ok(dbias))
+        return LEMO_ERR_INVALID_ARG;
+    if ((x != nullptr) == (checkpoint != nullptr)) return LEMO_ERR_INVALID_ARG;
+    if (x && (!mat_ok(x, ld_x, d) || x_rows < 0)) return LEMO_ERR_INVALID_ARG;
+    if (checkpoint && (e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
+    const bool sums = dweight || dbias;
+    if (sums && (!ws || !aligned(ws, 256) || ws_bytes < lemo_norm_workspace_size(d)))
+        return LEMO_ERR_INVALID_ARG;
+    lemo::norm::Args a = norm_args(norm, d, weight, nullptr, kept_idx, kept_total, rows);
+    a.x = vecs(dx);
+    a.ld_x = ld_dx / 8;
+    a.x_rows = dx_rows;
+    a.y = vecs(const_cast<uint16_t*>(dy));
+    a.ld_y = ld_dy / 8;
+    a.src = vecs(x);
+    a.ld_src = ld_x / 8;
+    a.src_rows = x_rows;
+    a.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
+    a.c = view_of(checkpoint);
+    a.part = sums ? static_cast<float*>(ws) : nullptr;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int grid = 0;
+    if ((e = run_norm<true, false>(a, st, &grid)) != LEMO_OK || !sums) return e;
+    return run_column_sums(a, grid, nullptr, nullptr, nullptr, dweight, dbias, nullptr, st);
+}
+
+lemo_status lemo_norm_scatter(lemo_norm norm, uint16_t* x, int64_t ld_x, int64_t x_rows, int32_t d,
+                              const uint16_t* y, int64_t ld_y, int64_t rows,
+                              const uint16_t* weight, const uint16_t* bias, float eps,
+                              const uint16_t* gate, int64_t ld_gate, float scale,
+                              const int32_t* kept_idx, const int32_t* kept_total, float* stats,
+                              const lemo_checkpoint* checkpoint, lemo_stream stream) {
+    lemo_status e = check_rows(rows, d, kept_idx, kept_total);
+    if (e != LEMO_OK) return e;
+    if (norm < LEMO_NORM_NONE || norm > LEMO_NORM_LAYER) return LEMO_ERR_INVALID_ARG;
+    if (norm == LEMO_NORM_NONE && (weight || bias || stats)) return LEMO_ERR_INVALID_ARG;
+    if (d > lemo::norm::kMaxD) return LEMO_ERR_UNSUPPORTED;
+    if (!mat_ok(x, ld_x, d) || !mat_ok(y, ld_y, d) || x_rows < 0 || !eps_ok(eps))
+        return LEMO_ERR_INVALID_ARG;
+    if (!vec_ok(weight) || !vec_ok(bias) || !aligned(stats, 8) || !(scale - scale == 0.f))
+        return LEMO_ERR_INVALID_ARG;
+    if (ld_gate != 0 && (!gate || ld_gate < d || ld_gate % 8 != 0)) return LEMO_ERR_INVALID_ARG;
+    if (!vec_ok(gate)) return LEMO_ERR_INVALID_ARG;
+    if (checkpoint && (e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
+    lemo::norm::Args a = norm_args(norm, d, weight, bias, kept_idx, kept_total, rows);
+    a.eps = eps;
+    a.scale = scale;
+    a.x = vecs(x);
+    a.ld_x = ld_x / 8;
+    a.x_rows = x_rows;
+    a.y = vecs(const_cast<uint16_t*>(y));
+    a.ld_y = ld_y / 8;
+    a.gate = vecs(gate);
+    a.ld_gate = ld_gate / 8;
+    a.stats = reinterpret_cast<float2*>(stats);
+    a.c = view_of(checkpoint);
+    int grid = 0;
+    return run_norm<false, true>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
+}
+
+lemo_status lemo_norm_scatter_backward(
+    lemo_norm norm, const uint16_t* dx, int64_t ld_dx, int64_t dx_rows, int32_t d,
+    const uint16_t* weight, const uint16_t* bias, const float* stats, const uint16_t* gate,
+    int64_t ld_gate, float scale, const int32_t* kept_idx, const int32_t* kept_total,
+    const uint16_t* y, int64_t ld_y, const lemo_checkpoint* checkpoint, int32_t pad_to,
+    uint16_t* dy, int64_t ld_dy, int64_t rows, float* dweight, float* dbias, float* dgate,
+    uint16_t* dgate_rows, int64_t ld_dgate_rows, void* ws, size_t ws_bytes, lemo_stream stream) {
+    lemo_status e = check_rows(rows, d, kept_idx, kept_total);
+    if (e != LEMO_OK) return e;
+    if (norm < LEMO_NORM_NONE || norm > LEMO_NORM_LAYER || pad_to < 1) return LEMO_ERR_INVALID_ARG;
+    if (norm == LEMO_NORM_NONE ? (weight || bias || dweight || dbias) : !stats)
+        return LEMO_ERR_INVALID_ARG;
+    if (d > lemo::norm::kMaxD) return LEMO_ERR_UNSUPPORTED;
+    if (!mat_ok(dx, ld_dx, d) || !mat_ok(dy, ld_dy, d) || dx_rows < 0) return LEMO_ERR_INVALID_ARG;
+    if (!aligned(stats, 8) || !vec_ok(weight) || !vec_ok(bias) || !f32_ok(dweight) ||
+        !f32_ok(dbias) || !f32_ok(dgate) || !(scale - scale == 0.f))
+        return LEMO_ERR_INVALID_ARG;
+    if (ld_gate != 0 && (!gate || ld_gate < d || ld_gate % 8 != 0)) return LEMO_ERR_INVALID_ARG;
+    if (!vec_ok(gate)) return LEMO_ERR_INVALID_ARG;
+    if (dgate && (!gate || ld_gate != 0)) return LEMO_ERR_INVALID_ARG;
+    if (dgate_rows && (ld_gate == 0 || !mat_ok(dgate_rows, ld_dgate_rows, d)))
+        return LEMO_ERR_INVALID_ARG;
+    if ((y != nullptr) == (checkpoint != nullptr)) return LEMO_ERR_INVALID_ARG;
+    if (y && !mat_ok(y, ld_y, d)) return LEMO_ERR_INVALID_ARG;
+    if (checkpoint && (e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
+    const bool sums = dweight || dbias || dgate;
+    if (sums && (!ws || !aligned(ws, 256) || ws_bytes < lemo_norm_workspace_size(d)))
+        return LEMO_ERR_INVALID_ARG;
+    lemo::norm::Args a = norm_args(norm, d, weight, bias, kept_idx, kept_total, rows);
+    a.scale = scale;
+    a.x = vecs(const_cast<uint16_t*>(dx));
+    a.ld_x = ld_dx / 8;
+    a.x_rows = dx_rows;
+    a.y = vecs(dy);
+    a.ld_y = ld_dy / 8;
+    a.src = vecs(y);
+    a.ld_src = ld_y / 8;
+    a.src_rows = rows;
+    a.gate = vecs(gate);
+    a.ld_gate = ld_gate / 8;
+    a.dgate_rows = vecs(dgate_rows);
+    a.ld_dgate = ld_dgate_rows / 8;
+    a.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
+    a.c = view_of(checkpoint);
+    a.pad_to = pad_to;
+    a.part = sums ? static_cast<float*>(ws) : nullptr;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int grid = 0;
+    if ((e = run_norm<true, true>(a, st, &grid)) != LEMO_OK || !sums) return e;
+    return run_column_sums(a, grid, weight, bias, ld_gate == 0 ? gate : nullptr, dweight, dbias,
+                           dgate, st);
+}
+
+lemo_status lemo_checkpoint_save(const uint16_t* x, int64_t ld_x, int64_t x_rows,
+                                 const int32_t* kept_idx, const int32_t* kept_total,
+                                 const lemo_checkpoint* checkpoint, lemo_stream stream) {
+    if (!checkpoint) return LEMO_ERR_INVALID_ARG;
+    const int32_t d = checkpoint->d;
+    lemo_status e = check_rows(checkpoint->rows, d, kept_idx, kept_total);
+    if (e != LEMO_OK) return e;
+    if ((e = check_checkpoint(checkpoint, d, 0)) != LEMO_OK) return e;
+    if (!mat_ok(x, ld_x, d) || x_rows < 0) return LEMO_ERR_INVALID_ARG;
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms <= 0) return LEMO_ERR_CUDA;
+    lemo::ckpt::RowsArgs a = {};
+    a.x = vecs(x);
+    a.ld = ld_x / 8;
+    a.x_rows = x_rows;
+    a.dvec = d / 8;
+    a.kept_idx = kept_idx;
+    a.kept_total = kept_total;
+    a.rows = checkpoint->rows;
+    a.c = view_of(checkpoint);
+    launch(lemo::ckpt::save_kernel, ckpt_grid(lemo::ckpt::save_kernel, sms, a.rows),
+           lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch_status();
+}
+
+lemo_status lemo_checkpoint_restore(const lemo_checkpoint* checkpoint, const int32_t* kept_total,
+                                    int32_t pad_to, uint16_t* y, int64_t ld_y, int64_t rows,
+                                    lemo_stream stream) {
+    if (!checkpoint) return LEMO_ERR_INVALID_ARG;
+    const int32_t d = checkpoint->d;
+    lemo_status e = check_rows(rows, d, nullptr, kept_total);
+    if (e != LEMO_OK) return e;
+    if ((e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
+    if (!mat_ok(y, ld_y, d) || pad_to < 1) return LEMO_ERR_INVALID_ARG;
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms <= 0) return LEMO_ERR_CUDA;
+    lemo::ckpt::RowsArgs a = {};
+    a.y = vecs(y);
+    a.ld = ld_y / 8;
+    a.dvec = d / 8;
+    a.kept_total = kept_total;
+    a.rows = rows;
+    a.pad_to = pad_to;
+    a.c = view_of(checkpoint);
+    launch(lemo::ckpt::restore_kernel, ckpt_grid(lemo::ckpt::restore_kernel, sms, rows),
+           lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch_status();
+}
+
+lemo_status lemo_gated_mlp(const uint16_t* gate, int64_t ld_gate, const uint16_t* up,
+                           int64_t ld_up, int32_t d, const int32_t* kept_total, int32_t pad_to,
+                           uint16_t* a_out, int64_t ld_a, int64_t rows,
+                           const lemo_checkpoint* gate_checkpoint,
+                           const lemo_checkpoint* up_checkpoint, lemo_stream stream) {
+    lemo_status e = check_rows(rows, d, nullptr, kept_total);
+    if (e != LEMO_OK) return e;
+    if (!mat_ok(gate, ld_gate, d) || !mat_ok(up, ld_up, d) || !mat_ok(a_out, ld_a, d) || pad_to < 1)
+        return LEMO_ERR_INVALID_ARG;
+    if (gate_checkpoint && (e = check_checkpoint(gate_checkpoint, d, rows)) != LEMO_OK) return e;
+    if (up_checkpoint && (e = check_checkpoint(up_checkpoint, d, rows)) != LEMO_OK) return e;
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms <= 0) return LEMO_ERR_CUDA;
+    lemo::ckpt::GatedArgs a = {};
+    a.g = vecs(gate);
+    a.ld_g = ld_gate / 8;
+    a.u = vecs(up);
+    a.ld_u = ld_up / 8;
+    a.a = vecs(a_out);
+    a.ld_a = ld_a / 8;
+    a.dvec = d / 8;
+    a.kept_total = kept_total;
+    a.rows = rows;
+    a.pad_to = pad_to;
+    a.cg = view_of(gate_checkpoint);
+    a.cu = view_of(up_checkpoint);
+    launch(lemo::ckpt::gated_kernel,
+           ckpt_grid(lemo::ckpt::gated_kernel, sms, rows * ((a.dvec + 31) / 32)),
+           lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch_status();
+}
+
+lemo_status lemo_gated_mlp_backward(const lemo_checkpoint* gate_checkpoint,
+                                    const lemo_checkpoint* up_checkpoint, const uint16_t* da,
+                                    int64_t ld_da, const int32_t* kept_total, int32_t pad_to,
+                                    uint16_t* dgate, int64_t ld_dgate, uint16_t* dup,
+                                    int64_t ld_dup, uint16_t* a_out, int64_t ld_a, int64_t rows,
+                                    lemo_stream stream) {
+    if (!gate_checkpoint || !up_checkpoint) return LEMO_ERR_INVALID_ARG;
+    const int32_t d = gate_checkpoint->d;
+    lemo_status e = check_rows(rows, d, nullptr, kept_total);
+    if (e != LEMO_OK) return e;
+    if ((e = check_checkpoint(gate_checkpoint, d, rows)) != LEMO_OK) return e;
+    if ((e = check_checkpoint(up_checkpoint, d, rows)) != LEMO_OK) return e;
+    if (!mat_ok(da, ld_da, d) || !mat_ok(dgate, ld_dgate, d) || !mat_ok(dup, ld_dup, d) ||
+        (a_out && !mat_ok(a_out, ld_a, d)) || pad_to < 1)
+        return LEMO_ERR_INVALID_ARG;
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms <= 0) return LEMO_ERR_CUDA;
+    lemo::ckpt::GatedArgs a = {};
+    a.da = vecs(da);
+    a.ld_da = ld_da / 8;
+    a.dg = vecs(dgate);
+    a.ld_dg = ld_dgate / 8;
+    a.du = vecs(dup);
+    a.ld_du = ld_dup / 8;
+    a.a = vecs(a_out);
+    a.ld_a = ld_a / 8;
+    a.dvec = d / 8;
+    a.kept_total = kept_total;
+    a.rows = rows;
+    a.pad_to = pad_to;
+    a.cg = view_of(gate_checkpoint);
+    a.cu = view_of(up_checkpoint);
+    launch(lemo::ckpt::gated_backward_kernel,
+           ckpt_grid(lemo::ckpt::gated_backward_kernel, sms, rows * ((a.dvec + 31) / 32)),
+           lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch_status();
+}
+
+lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const uint16_t* dy,
+                                        int64_t ld_dy, int64_t rows, int32_t n,
+                                        const int32_t* kept_total, float* dw, int64_t ld_dw,
+                                        lemo_stream stream) {
+    if (!checkpoint) return LEMO_ERR_INVALID_ARG;
+    const int32_t d = checkpoint->d;
+    lemo_status e = check_rows(rows, d, nullptr, kept_total);
+    if (e != LEMO_OK) return e;
+    if ((e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
+    if (n < 1) return LEMO_ERR_INVALID_ARG;
+    if (n % 8 != 0) return LEMO_ERR_UNSUPPORTED;
+    if (!mat_ok(dy, ld_dy, n) || !dw || !aligned(dw, 16) || ld_dw < d || ld_dw % 4 != 0)
+        return LEMO_ERR_INVALID_ARG;
+    namespace wg = lemo::wgrad;
+    wg::Args a = {};
+    a.c = view_of(checkpoint);
+    a.dy = dy;
+    a.ld_dy = ld_dy;
+    a.dw = dw;
+    a.ld_dw = ld_dw;
+    a.n = n;
+    a.d = d;
+    a.kept_total = kept_total;
+    a.rows = rows;
+    launch(wg::simple_kernel,
+           dim3((unsigned)((d + wg::kTile - 1) / wg::kTile), (unsigned)((n + wg::kTile - 1) / wg::kTile)),
+           256, 0, reinterpret_cast<cudaStream_t>(stream), a);
     return launch_status();
 }
 

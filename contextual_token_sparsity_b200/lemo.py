@@ -42,6 +42,24 @@ class lemo_shape(ctypes.Structure):
     ]
 
 
+class lemo_checkpoint(ctypes.Structure):
+    _fields_ = [
+        ("format", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+        ("ld_data", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("ld_scales", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+    ]
+
+
+LEMO_NORM_NONE = 0
+LEMO_NORM_RMS = 1
+LEMO_NORM_LAYER = 2
+LEMO_CHECKPOINT_E4M3 = 0
+LEMO_CHECKPOINT_INT8 = 1
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -72,6 +90,26 @@ _SIGS = {
     "lemo_segment_loss_workspace_size": (ctypes.c_size_t, [_I64, _I32, _I32]),
     "lemo_segment_loss": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _I64, _I32, _P, _I32, _I32, _P,
                                          _P, _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P]),
+    "lemo_norm_gather": (ctypes.c_int, [_I32, _P, _I64, _I64, _I32, _P, _P, ctypes.c_float, _P, _P,
+                                        _I32, _P, _I64, _I64, _P, _P, _P]),
+    "lemo_norm_workspace_size": (ctypes.c_size_t, [_I32]),
+    "lemo_norm_gather_backward": (ctypes.c_int, [_I32, _P, _I64, _I64, _I32, _P, _P, _P, _P, _P,
+                                                 _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P,
+                                                 ctypes.c_size_t, _P]),
+    "lemo_norm_scatter": (ctypes.c_int, [_I32, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _P,
+                                         ctypes.c_float, _P, _I64, ctypes.c_float, _P, _P, _P, _P,
+                                         _P]),
+    "lemo_norm_scatter_backward": (ctypes.c_int, [_I32, _P, _I64, _I64, _I32, _P, _P, _P, _P, _I64,
+                                                  ctypes.c_float, _P, _P, _P, _I64, _P, _I32, _P,
+                                                  _I64, _I64, _P, _P, _P, _P, _I64, _P,
+                                                  ctypes.c_size_t, _P]),
+    "lemo_checkpoint_save": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P]),
+    "lemo_checkpoint_restore": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _I64, _P]),
+    "lemo_gated_mlp": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I32, _P, _I64, _I64, _P, _P,
+                                      _P]),
+    "lemo_gated_mlp_backward": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I32, _P, _I64, _P, _I64, _P,
+                                               _I64, _I64, _P]),
+    "lemo_checkpoint_weight_grad": (ctypes.c_int, [_P, _P, _I64, _I64, _I32, _P, _P, _I64, _P]),
     "lemo_get_error": (ctypes.c_int, [_P]),
     "lemo_set_test_hooks": (None, [_I32, _I64]),
     "lemo_set_predict_test_hook": (None, [_I32]),
@@ -251,6 +289,273 @@ def lemo_segment_loss(h, w, targets, seg_rows, loss, ws, token_loss=None, dh=Non
         dh.stride(0) if dh is not None else 0, _ptr(dw), dw.stride(0) if dw is not None else 0,
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
         "lemo_segment_loss")
+
+
+# ---------------------------------------------------------------------------
+# Norms around a sublayer and 8-bit checkpoints.  These calls take tensors
+# (not addresses) and check, before anything is enqueued, that each one is on
+# the current CUDA device and has the type, row layout and sizes the call
+# needs; a tensor that does not fit raises LemoError(LEMO_ERR_INVALID_ARG).
+# ---------------------------------------------------------------------------
+class _Fit:
+    """Tensor checks of one call: ``fit(...)`` returns the data pointer."""
+
+    __slots__ = ("where", "dev")
+
+    def __init__(self, where: str):
+        import torch
+        self.where = where
+        self.dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+    def _bad(self, name, why):
+        err = LemoError(LEMO_ERR_INVALID_ARG, self.where)
+        err.args = (f"{self.where}: {name} {why}",)
+        raise err
+
+    def mat(self, t, name, dtype, cols, rows=0):
+        if t is None:
+            self._bad(name, "is missing")
+        if str(t.dtype) != dtype or t.dim() != 2:
+            self._bad(name, f"is not a 2-D {dtype} tensor")
+        if t.get_device() != self.dev:
+            self._bad(name, "is not on the current CUDA device")
+        n, width = t.shape
+        if n < rows or width < cols:
+            self._bad(name, f"has shape {(n, width)}, at least {(rows, cols)} is needed")
+        if width > 1 and t.stride(1) != 1:
+            self._bad(name, "does not have contiguous rows")
+        return t.data_ptr()
+
+    def vec(self, t, name, dtype, n):
+        if t is None:
+            return None
+        if str(t.dtype) != dtype or t.dim() != 1 or t.shape[0] < n:
+            self._bad(name, f"is not a 1-D {dtype} tensor of at least {n} values")
+        if t.get_device() != self.dev:
+            self._bad(name, "is not on the current CUDA device")
+        if n > 1 and t.stride(0) != 1:
+            self._bad(name, "is not contiguous")
+        return t.data_ptr()
+
+    def idx(self, kept_idx, kept_total):
+        if kept_total is None:
+            self._bad("kept_total", "is missing")
+        return (self.vec(kept_idx, "kept_idx", _INT32, 0),
+                self.vec(kept_total, "kept_total", _INT32, 1))
+
+    def ckpt(self, c, name, d, rows):
+        if c is None:
+            return None
+        if not isinstance(c, Checkpoint):
+            self._bad(name, "is not a Checkpoint")
+        if c.device != self.dev:
+            self._bad(name, "is not on the current CUDA device")
+        if c.d != d or c.rows < rows:
+            self._bad(name, f"holds {(c.rows, c.d)}, at least {(rows, d)} is needed")
+        return c.ref
+
+
+_BF16, _FP32, _INT32, _UINT8 = "torch.bfloat16", "torch.float32", "torch.int32", "torch.uint8"
+
+
+def _ld(t, unit=8):
+    """Row stride of a 2-D tensor (a single row's own stride says nothing)."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
+
+
+class Checkpoint:
+    """Rows in 8 bits: ``data`` uint8 [rows, >= d] (row stride a multiple of 16
+    bytes), ``scales`` uint8 [rows, >= ceil(d / 32)] (a multiple of 4)."""
+
+    def __init__(self, data, scales, format: int, d: int):
+        fit = _Fit("make_checkpoint")
+        fit.mat(data, "data", _UINT8, d)
+        fit.mat(scales, "scales", _UINT8, -(-d // 32), data.shape[0])
+        self.data, self.scales, self.d, self.rows = data, scales, int(d), data.shape[0]
+        self.device = data.get_device()
+        self.struct = lemo_checkpoint(int(format), int(d), data.data_ptr(), _ld(data, 16),
+                                      scales.data_ptr(), _ld(scales, 4), data.shape[0])
+        self.ref = ctypes.addressof(self.struct)
+
+
+def make_checkpoint(data, scales, format: int, d: int) -> Checkpoint:
+    """Checkpoint handle over two uint8 tensors (kept alive by the handle)."""
+    return Checkpoint(data, scales, format, d)
+
+
+def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y, stats=None,
+                     checkpoint=None, stream=None, d=None):
+    """x bf16 [x_rows, >= d], y bf16 [rows, >= d], weight / bias bf16 [d] or
+    None, stats fp32 [rows, 2] contiguous, kept_idx int32 (at least K) or None."""
+    fit = _Fit("lemo_norm_gather")
+    d = x.shape[1] if d is None else d
+    xp, yp, rows = fit.mat(x, "x", _BF16, d), fit.mat(y, "y", _BF16, d), y.shape[0]
+    ip, kp = fit.idx(kept_idx, kept_total)
+    _check(load().lemo_norm_gather(
+        int(norm), xp, _ld(x), x.shape[0], int(d), fit.vec(weight, "weight", _BF16, d),
+        fit.vec(bias, "bias", _BF16, d), float(eps), ip, kp, int(pad_to), yp, _ld(y), rows,
+        _stats(fit, stats, rows), fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
+        "lemo_norm_gather")
+
+
+def _stats(fit, stats, rows):
+    if stats is None:
+        return None
+    p = fit.mat(stats, "stats", _FP32, 2, rows)
+    if stats.shape[1] != 2 or (rows > 1 and stats.stride(0) != 2):
+        fit._bad("stats", "is not a contiguous [rows, 2] tensor")
+    return p
+
+
+def _workspace(fit, ws, needed):
+    if ws is None:
+        if needed:
+            fit._bad("ws", "is missing")
+        return None, 0
+    if ws.get_device() != fit.dev or not ws.is_contiguous():
+        fit._bad("ws", "is not a contiguous tensor on the current CUDA device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def lemo_norm_workspace_size(d: int) -> int:
+    return int(load().lemo_norm_workspace_size(int(d)))
+
+
+def lemo_norm_gather_backward(norm, dy, weight, stats, kept_idx, kept_total, dx, ws, x=None,
+                              checkpoint=None, dweight=None, dbias=None, stream=None, d=None):
+    """dy bf16 [rows, >= d], dx bf16 [tokens, >= d] (updated in place); exactly
+    one of x (the forward call's input) and checkpoint; dweight / dbias fp32
+    [d] optional (accumulated); ws may be None without them."""
+    fit = _Fit("lemo_norm_gather_backward")
+    d = dy.shape[1] if d is None else d
+    rows = dy.shape[0]
+    dyp, dxp = fit.mat(dy, "dy", _BF16, d), fit.mat(dx, "dx", _BF16, d)
+    ip, kp = fit.idx(kept_idx, kept_total)
+    wsp, ws_bytes = _workspace(fit, ws, dweight is not None or dbias is not None)
+    _check(load().lemo_norm_gather_backward(
+        int(norm), dyp, _ld(dy), rows, int(d), fit.vec(weight, "weight", _BF16, d),
+        _stats(fit, stats, rows), ip, kp, None if x is None else fit.mat(x, "x", _BF16, d),
+        _ld(x), 0 if x is None else x.shape[0], fit.ckpt(checkpoint, "checkpoint", d, rows),
+        dxp, _ld(dx), dx.shape[0], fit.vec(dweight, "dweight", _FP32, d),
+        fit.vec(dbias, "dbias", _FP32, d), wsp, ws_bytes, _stream(stream)),
+        "lemo_norm_gather_backward")
+
+
+def _gate(fit, gate, d, rows):
+    if gate is None:
+        return None, 0
+    if gate.dim() == 1:
+        return fit.vec(gate, "gate", _BF16, d), 0
+    return fit.mat(gate, "gate", _BF16, d, rows), _ld(gate)
+
+
+def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept_total,
+                      stats=None, checkpoint=None, stream=None, d=None):
+    """x bf16 [tokens, >= d] (updated in place), y bf16 [rows, >= d]; gate None,
+    bf16 [d] (all tokens) or bf16 [rows, >= d] (per kept row)."""
+    fit = _Fit("lemo_norm_scatter")
+    d = x.shape[1] if d is None else d
+    rows = y.shape[0]
+    xp, yp = fit.mat(x, "x", _BF16, d), fit.mat(y, "y", _BF16, d)
+    ip, kp = fit.idx(kept_idx, kept_total)
+    gp, ld_gate = _gate(fit, gate, d, rows)
+    _check(load().lemo_norm_scatter(
+        int(norm), xp, _ld(x), x.shape[0], int(d), yp, _ld(y), rows,
+        fit.vec(weight, "weight", _BF16, d), fit.vec(bias, "bias", _BF16, d), float(eps), gp,
+        ld_gate, float(scale), ip, kp, _stats(fit, stats, rows),
+        fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
+        "lemo_norm_scatter")
+
+
+def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_idx, kept_total,
+                               pad_to, dy, ws, y=None, checkpoint=None, dweight=None, dbias=None,
+                               dgate=None, stream=None, d=None):
+    """dx bf16 [tokens, >= d] (read), dy bf16 [rows, >= d] (written); exactly one
+    of y and checkpoint; dgate fp32 [d] (accumulated) for a gate of one row,
+    bf16 [rows, >= d] (written) for a gate row per kept row."""
+    fit = _Fit("lemo_norm_scatter_backward")
+    d = dx.shape[1] if d is None else d
+    rows = dy.shape[0]
+    dxp, dyp = fit.mat(dx, "dx", _BF16, d), fit.mat(dy, "dy", _BF16, d)
+    ip, kp = fit.idx(kept_idx, kept_total)
+    gp, ld_gate = _gate(fit, gate, d, rows)
+    per_row = dgate is not None and dgate.dim() == 2
+    dg = None if per_row else fit.vec(dgate, "dgate", _FP32, d)
+    dgr = fit.mat(dgate, "dgate", _BF16, d, rows) if per_row else None
+    wsp, ws_bytes = _workspace(fit, ws, dweight is not None or dbias is not None or dg is not None)
+    _check(load().lemo_norm_scatter_backward(
+        int(norm), dxp, _ld(dx), dx.shape[0], int(d), fit.vec(weight, "weight", _BF16, d),
+        fit.vec(bias, "bias", _BF16, d), _stats(fit, stats, rows), gp, ld_gate, float(scale), ip,
+        kp, None if y is None else fit.mat(y, "y", _BF16, d, rows), _ld(y),
+        fit.ckpt(checkpoint, "checkpoint", d, rows), int(pad_to), dyp, _ld(dy), rows,
+        fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), dg, dgr,
+        _ld(dgate) if per_row else 0, wsp, ws_bytes, _stream(stream)),
+        "lemo_norm_scatter_backward")
+
+
+def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
+    """x bf16 [tokens, >= checkpoint.d]; kept_idx int32 or None (row r is token r)."""
+    fit = _Fit("lemo_checkpoint_save")
+    d = checkpoint.d
+    ip, kp = fit.idx(kept_idx, kept_total)
+    _check(load().lemo_checkpoint_save(fit.mat(x, "x", _BF16, d), _ld(x), x.shape[0], ip, kp,
+                                       fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream)),
+           "lemo_checkpoint_save")
+
+
+def lemo_checkpoint_restore(checkpoint, kept_total, pad_to, y, stream=None):
+    """y bf16 [rows, >= checkpoint.d], rows <= checkpoint.rows."""
+    fit = _Fit("lemo_checkpoint_restore")
+    d = checkpoint.d
+    _, kp = fit.idx(None, kept_total)
+    yp = fit.mat(y, "y", _BF16, d)
+    _check(load().lemo_checkpoint_restore(fit.ckpt(checkpoint, "checkpoint", d, y.shape[0]), kp,
+                                          int(pad_to), yp, _ld(y), y.shape[0], _stream(stream)),
+           "lemo_checkpoint_restore")
+
+
+def lemo_gated_mlp(gate, up, kept_total, pad_to, a, gate_checkpoint=None, up_checkpoint=None,
+                   stream=None, d=None):
+    """gate, up, a bf16 [rows, >= d]; a = SiLU(gate) up."""
+    fit = _Fit("lemo_gated_mlp")
+    d = a.shape[1] if d is None else d
+    rows = a.shape[0]
+    _, kp = fit.idx(None, kept_total)
+    _check(load().lemo_gated_mlp(
+        fit.mat(gate, "gate", _BF16, d, rows), _ld(gate), fit.mat(up, "up", _BF16, d, rows),
+        _ld(up), int(d), kp, int(pad_to), fit.mat(a, "a", _BF16, d), _ld(a), rows,
+        fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
+        fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), _stream(stream)),
+        "lemo_gated_mlp")
+
+
+def lemo_gated_mlp_backward(gate_checkpoint, up_checkpoint, da, kept_total, pad_to, dgate, dup,
+                            a=None, stream=None):
+    """da, dgate, dup and the optional recomputed activation a: bf16 [rows, >= d]."""
+    fit = _Fit("lemo_gated_mlp_backward")
+    d, rows = gate_checkpoint.d, dgate.shape[0]
+    _, kp = fit.idx(None, kept_total)
+    _check(load().lemo_gated_mlp_backward(
+        fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
+        fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), fit.mat(da, "da", _BF16, d, rows),
+        _ld(da), kp, int(pad_to), fit.mat(dgate, "dgate", _BF16, d), _ld(dgate),
+        fit.mat(dup, "dup", _BF16, d, rows), _ld(dup),
+        None if a is None else fit.mat(a, "a", _BF16, d, rows), _ld(a), rows, _stream(stream)),
+        "lemo_gated_mlp_backward")
+
+
+def lemo_checkpoint_weight_grad(checkpoint, dy, kept_total, dw, stream=None, n=None):
+    """dw fp32 [n, >= d] += dy^T xhat; dy bf16 [rows, >= n], n = dy's width."""
+    fit = _Fit("lemo_checkpoint_weight_grad")
+    d, rows = checkpoint.d, dy.shape[0]
+    n = dy.shape[1] if n is None else n
+    _, kp = fit.idx(None, kept_total)
+    _check(load().lemo_checkpoint_weight_grad(
+        fit.ckpt(checkpoint, "checkpoint", d, rows), fit.mat(dy, "dy", _BF16, n), _ld(dy), rows,
+        int(n), kp, fit.mat(dw, "dw", _FP32, d, n), _ld(dw, 4), _stream(stream)),
+        "lemo_checkpoint_weight_grad")
 
 
 def lemo_get_error(stream=None) -> int:

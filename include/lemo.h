@@ -490,6 +490,232 @@ LEMO_API lemo_status lemo_segment_loss(const uint16_t* h, int64_t ld_h, int64_t 
                                        uint16_t* dh, int64_t ld_dh, float* dw, int64_t ld_dw,
                                        void* ws, size_t ws_bytes, lemo_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Norms around a sublayer and 8-bit activation checkpoints (extensions of
+ * steps a6-a7 to what a sublayer does right after the selective load and
+ * right before the in-place addition, and to what its backward pass keeps).
+ *
+ * Shared rules:
+ *  - bf16 matrices are row-major with a row stride ("ld") in elements that is
+ *    a multiple of 8 and at least their width; matrices are 16-byte aligned;
+ *    vectors of d bf16 values are 16-byte aligned.
+ *  - `rows` is the number of rows of every buffer that is indexed by kept row
+ *    (each may have more).  If *kept_total, or the end of a zero tail, is
+ *    larger, only the first `rows` rows are processed and LEMO_ERR_CAPACITY is
+ *    recorded.
+ *  - kept_idx may be NULL: kept row r is then token r.
+ *  - Calls that update token rows in place need kept_idx strictly ascending,
+ *    as lemo_select writes it; an id that is out of range or not above the one
+ *    before it is recorded as LEMO_ERR_INVALID_ARG and its row is skipped.
+ *  - Zero tails: outputs that feed a GEMM over padded rows are written with
+ *    zeros in rows [K, round_up(K, pad_to)); rows beyond are not touched.
+ *  - Weight gradients are fp32 and ACCUMULATED (zero them for a fresh one);
+ *    every sum is taken in fp32 in a fixed order (deterministic).
+ *  - Different arguments of one call must not overlap.
+ * --------------------------------------------------------------------- */
+
+typedef enum lemo_norm {
+    LEMO_NORM_NONE = 0,   /* lemo_norm_scatter(_backward) only            */
+    LEMO_NORM_RMS = 1,    /* v / sqrt(mean(v^2) + eps)                    */
+    LEMO_NORM_LAYER = 2   /* (v - mean(v)) / sqrt(var(v) + eps)           */
+} lemo_norm;
+
+typedef enum lemo_checkpoint_format {
+    LEMO_CHECKPOINT_E4M3 = 0,  /* 8-bit float, 3 mantissa bits, largest 448 */
+    LEMO_CHECKPOINT_INT8 = 1   /* -127 .. 127                               */
+} lemo_checkpoint_format;
+
+/*
+ * Rows of bf16 values held in 8 bits.  Every 32 columns of a row (the last
+ * group of a row may be short) share a power-of-two scale 2^k, stored as the
+ * byte k + 127; k is the smallest integer >= -124 for which the group's
+ * largest magnitude divided by 2^k is at most 448 (E4M3) or 127 (INT8).  A
+ * value's code is value / 2^k rounded to nearest even (the division is
+ * exact), so nothing saturates; code x 2^k is exact in bf16.  (Next to bf16's
+ * largest value a code that would stand for 2^128 is taken one lower, 240 x
+ * 2^120 or 63 x 2^122.)  A group that holds an infinity or a NaN stores the
+ * scale byte 255 and restores as NaN.
+ */
+typedef struct lemo_checkpoint {
+    int32_t format;      /* lemo_checkpoint_format                                    */
+    int32_t d;           /* values per row, d % 8 == 0                                */
+    uint8_t* data;       /* DEVICE [rows, ld_data] codes, 16-byte aligned             */
+    int64_t ld_data;     /* bytes, multiple of 16, >= d                               */
+    uint8_t* scales;     /* DEVICE [rows, ld_scales] scale bytes, 4-byte aligned      */
+    int64_t ld_scales;   /* bytes, multiple of 4, >= ceil(d / 32)                     */
+    int64_t rows;        /* rows of data and scales                                   */
+} lemo_checkpoint;
+
+/*
+ * Selective load fused with the norm before the sublayer.
+ *
+ * Jenga summary, section 4.2.3, "Selective Load" (the gather); the sublayers
+ * of the models it trains start with a norm.
+ *
+ *   t = kept_idx[r], v = x[t, 0:d], vhat = (v - mean) rstd         (mean = 0 for RMS)
+ *   y[r] = bf16(vhat weight + bias)  for r < K, zero tail as lemo_gather_pad
+ *
+ * norm        LEMO_NORM_RMS or LEMO_NORM_LAYER.
+ * x           DEVICE bf16 [x_rows, ld_x].   d <= 16384, d % 8 == 0.
+ * weight, bias  DEVICE bf16 [d] or NULL (ones, zeros).   eps >= 0.
+ * y           DEVICE bf16 [rows, ld_y].
+ * stats       optional DEVICE fp32 [rows, 2]: (mean, rstd) of each kept row,
+ *             8-byte aligned; the backward pass needs it.
+ * checkpoint  optional: x[t] is also saved there as row r (checkpoint->d = d,
+ *             checkpoint->rows >= rows).
+ * One pass over x.  Ids may repeat or come in any order.
+ */
+LEMO_API lemo_status lemo_norm_gather(lemo_norm norm, const uint16_t* x, int64_t ld_x,
+                                      int64_t x_rows, int32_t d, const uint16_t* weight,
+                                      const uint16_t* bias, float eps, const int32_t* kept_idx,
+                                      const int32_t* kept_total, int32_t pad_to, uint16_t* y,
+                                      int64_t ld_y, int64_t rows, float* stats,
+                                      const lemo_checkpoint* checkpoint, lemo_stream stream);
+
+/*
+ * Workspace bytes of the two norm backward calls for rows of d values (the
+ * per-CTA column sums).  Returns 0 for an invalid d.  HOST-only computation.
+ */
+LEMO_API size_t lemo_norm_workspace_size(int32_t d);
+
+/*
+ * Backward of lemo_norm_gather.  With vhat from the row's source and stats:
+ *
+ *   g = dy[r] weight,  dv = rstd (g - vhat mean(g vhat) [- mean(g) for LAYER])
+ *   dx[kept_idx[r]] = bf16(dx[kept_idx[r]] + dv)      (in place; ids strictly ascending)
+ *   dweight += sum_r dy[r] vhat,   dbias += sum_r dy[r]
+ *
+ * dy          DEVICE bf16 [rows, ld_dy]; rows >= K are not read.
+ * x           DEVICE bf16 [x_rows, ld_x], the forward call's input rows, or
+ *             NULL with `checkpoint` given (exactly one of the two): vhat then
+ *             comes from the checkpointed values.
+ * stats       DEVICE fp32 [rows, 2] from the forward call.
+ * dx          DEVICE bf16 [dx_rows, ld_dx], the residual gradient.
+ * dweight, dbias  optional DEVICE fp32 [d].
+ * ws          DEVICE, lemo_norm_workspace_size(d) bytes, 256-byte aligned; may
+ *             be NULL when dweight and dbias are.
+ */
+LEMO_API lemo_status lemo_norm_gather_backward(
+    lemo_norm norm, const uint16_t* dy, int64_t ld_dy, int64_t rows, int32_t d,
+    const uint16_t* weight, const float* stats, const int32_t* kept_idx,
+    const int32_t* kept_total, const uint16_t* x, int64_t ld_x, int64_t x_rows,
+    const lemo_checkpoint* checkpoint, uint16_t* dx, int64_t ld_dx, int64_t dx_rows,
+    float* dweight, float* dbias, void* ws, size_t ws_bytes, lemo_stream stream);
+
+/*
+ * The norm after the sublayer, its gate and the residual scale fused with the
+ * in-place addition (Jenga summary, section 4.2.3, "In-place Addition").
+ *
+ *   v = y[r], n = vhat weight + bias        (LEMO_NORM_NONE: n = v, weight = bias = NULL)
+ *   x[kept_idx[r]] = bf16(x[kept_idx[r]] + scale gate n)  (in place; ids strictly ascending)
+ *
+ * gate        DEVICE bf16: ld_gate = 0, one row of d values for all tokens
+ *             (layer scale), or ld_gate >= d, a row per kept row [rows,
+ *             ld_gate]; NULL: 1.
+ * scale       finite.
+ * stats, checkpoint  optional outputs: (mean, rstd) and the 8-bit copy of y[r].
+ * With LEMO_NORM_NONE stats must be NULL.
+ */
+LEMO_API lemo_status lemo_norm_scatter(lemo_norm norm, uint16_t* x, int64_t ld_x, int64_t x_rows,
+                                       int32_t d, const uint16_t* y, int64_t ld_y, int64_t rows,
+                                       const uint16_t* weight, const uint16_t* bias, float eps,
+                                       const uint16_t* gate, int64_t ld_gate, float scale,
+                                       const int32_t* kept_idx, const int32_t* kept_total,
+                                       float* stats, const lemo_checkpoint* checkpoint,
+                                       lemo_stream stream);
+
+/*
+ * Backward of lemo_norm_scatter.  The residual gradient dx passes to the
+ * layer's input unchanged and is only read.  With dz = scale dx[kept_idx[r]]
+ * and dn = dz gate:
+ *
+ *   dy[r] = bf16(rstd (dn weight - vhat mean(dn weight vhat) [- mean(dn weight)]))
+ *   dweight += sum_r dn vhat,   dbias += sum_r dn
+ *   dgate   += sum_r dz n                 (ld_gate = 0)
+ *   dgate_rows[r] = bf16(dz n)            (ld_gate > 0)
+ *
+ * y           DEVICE bf16 [rows, ld_y], the forward call's input, or NULL with
+ *             `checkpoint` given (exactly one of the two).
+ * dy          DEVICE bf16 [rows, ld_dy], zero tail as lemo_gather_pad.
+ * dweight, dbias, dgate  optional DEVICE fp32 [d] (NULL with LEMO_NORM_NONE: dweight, dbias).
+ * dgate_rows  optional DEVICE bf16 [rows, ld_dgate_rows]; rows >= K are not touched.
+ * Ids may repeat or come in any order (nothing is updated by token).
+ */
+LEMO_API lemo_status lemo_norm_scatter_backward(
+    lemo_norm norm, const uint16_t* dx, int64_t ld_dx, int64_t dx_rows, int32_t d,
+    const uint16_t* weight, const uint16_t* bias, const float* stats, const uint16_t* gate,
+    int64_t ld_gate, float scale, const int32_t* kept_idx, const int32_t* kept_total,
+    const uint16_t* y, int64_t ld_y, const lemo_checkpoint* checkpoint, int32_t pad_to,
+    uint16_t* dy, int64_t ld_dy, int64_t rows, float* dweight, float* dbias, float* dgate,
+    uint16_t* dgate_rows, int64_t ld_dgate_rows, void* ws, size_t ws_bytes, lemo_stream stream);
+
+/*
+ * Saves the rows x[kept_idx[r]], r < K, in 8 bits as rows r of `checkpoint`
+ * (rows beyond are not touched).  x: DEVICE bf16 [x_rows, ld_x], d =
+ * checkpoint->d.  Ids may repeat or come in any order.
+ */
+LEMO_API lemo_status lemo_checkpoint_save(const uint16_t* x, int64_t ld_x, int64_t x_rows,
+                                          const int32_t* kept_idx, const int32_t* kept_total,
+                                          const lemo_checkpoint* checkpoint, lemo_stream stream);
+
+/*
+ * Brings a checkpoint's rows back: y[r] = the bf16 values of row r (exact)
+ * for r < K, zero tail as lemo_gather_pad.  y: DEVICE bf16 [rows, ld_y],
+ * rows <= checkpoint->rows.
+ */
+LEMO_API lemo_status lemo_checkpoint_restore(const lemo_checkpoint* checkpoint,
+                                             const int32_t* kept_total, int32_t pad_to,
+                                             uint16_t* y, int64_t ld_y, int64_t rows,
+                                             lemo_stream stream);
+
+/*
+ * The SiLU-gated activation of an MLP with its inputs checkpointed in the same pass
+ * (the activation of the "Extend to MLP Block" scores, Jenga summary, section 4.2.1):
+ *
+ *   a[r] = bf16(SiLU(gate[r]) up[r]),  SiLU(g) = g / (1 + e^-g),  r < K, zero tail
+ *
+ * gate, up, a  DEVICE bf16 [rows, ld_*], d values per row.
+ * gate_checkpoint, up_checkpoint  optional outputs (d, rows >= rows).
+ */
+LEMO_API lemo_status lemo_gated_mlp(const uint16_t* gate, int64_t ld_gate, const uint16_t* up,
+                                    int64_t ld_up, int32_t d, const int32_t* kept_total,
+                                    int32_t pad_to, uint16_t* a, int64_t ld_a, int64_t rows,
+                                    const lemo_checkpoint* gate_checkpoint,
+                                    const lemo_checkpoint* up_checkpoint, lemo_stream stream);
+
+/*
+ * Backward of lemo_gated_mlp from the checkpointed g and u, s = 1 / (1 + e^-g):
+ *
+ *   dgate[r] = bf16(da u s (1 + g (1 - s))),  dup[r] = bf16(da g s),
+ *   a[r] = bf16(g s u)   (optional: the activation again, for the weight gradient after it)
+ *
+ * for r < K, zero tails.  da, dgate, dup, a: DEVICE bf16 [rows, ld_*]; both
+ * checkpoints have the same d and at least `rows` rows.
+ */
+LEMO_API lemo_status lemo_gated_mlp_backward(const lemo_checkpoint* gate_checkpoint,
+                                             const lemo_checkpoint* up_checkpoint,
+                                             const uint16_t* da, int64_t ld_da,
+                                             const int32_t* kept_total, int32_t pad_to,
+                                             uint16_t* dgate, int64_t ld_dgate, uint16_t* dup,
+                                             int64_t ld_dup, uint16_t* a, int64_t ld_a,
+                                             int64_t rows, lemo_stream stream);
+
+/*
+ * Weight gradient of a linear layer y = xhat W^T whose input is checkpointed:
+ *
+ *   dw[j, c] += sum_{r < K} dy[r, j] xhat[r, c]
+ *
+ * checkpoint  the input rows (d columns, at least `rows` rows).
+ * dy          DEVICE bf16 [rows, ld_dy], n values per row, n % 8 == 0; rows >= K
+ *             are not used, whatever they hold.
+ * dw          DEVICE fp32 [n, ld_dw], 16-byte aligned, ld_dw >= d a multiple of 4.
+ * The 8-bit values are exact in bf16; products accumulate in fp32.
+ */
+LEMO_API lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint,
+                                                 const uint16_t* dy, int64_t ld_dy, int64_t rows,
+                                                 int32_t n, const int32_t* kept_total, float* dw,
+                                                 int64_t ld_dw, lemo_stream stream);
+
 /*
  * Synchronises `stream`, then reports and clears the device error word of the
  * current device: LEMO_OK, LEMO_ERR_INVALID_ARG (cu_seqlens or an index
