@@ -1233,6 +1233,53 @@ lemo::norm::Args norm_args(lemo_norm norm, int32_t d, const uint16_t* w, const u
 
 bool eps_ok(float eps) { return eps >= 0.f && eps < __builtin_inff(); }
 
+// 2-D tensor map of a checkpoint's codes [rows, d] (bytes), boxes of 128
+// columns x 64 rows, not swizzled.
+bool encode_codes(CUtensorMap* tm, const lemo_checkpoint* c) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)c->d, (cuuint64_t)c->rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)c->ld_data};
+    const cuuint32_t box[2] = {(cuuint32_t)lemo::wgrad::HALF, (cuuint32_t)lemo::wgrad::KB};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->data, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// CTA pairs of the weight-gradient kernel that fit at once.
+int g_wgrad_pairs[kMaxDevices];
+
+int wgrad_pairs(int dev, int sms) {
+    namespace wg = lemo::wgrad;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (g_wgrad_pairs[dev] == 0) {
+        if (cudaFuncSetAttribute(wg::wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 wg::SMEM_BYTES) != cudaSuccess)
+            return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+        cfg.blockDim = dim3(wg::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = wg::SMEM_BYTES;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, wg::wgrad_kernel, &cfg) != cudaSuccess ||
+            clusters < 1) {
+            cudaGetLastError();
+            clusters = sms / 2;
+        }
+        g_wgrad_pairs[dev] = clusters < sms / 2 ? clusters : sms / 2;
+    }
+    return g_wgrad_pairs[dev];
+}
+
 // Persistent grid of the element-wise checkpoint kernels.
 template <typename Kernel>
 int ckpt_grid(Kernel, int sms, int64_t warps) {
@@ -1541,20 +1588,34 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     if (n % 8 != 0) return LEMO_ERR_UNSUPPORTED;
     if (!mat_ok(dy, ld_dy, n) || !dw || !aligned(dw, 16) || ld_dw < d || ld_dw % 4 != 0)
         return LEMO_ERR_INVALID_ARG;
+    if (rows == 0) return LEMO_OK;
     namespace wg = lemo::wgrad;
+    int dev = 0;
+    const int sms = device_sms(&dev);
+    if (sms <= 0) return LEMO_ERR_CUDA;
+    CUtensorMap tm_dy, tm_q, tm_dw;
+    if (!encode_operand(&tm_dy, dy, rows, n, ld_dy, true) || !encode_codes(&tm_q, checkpoint) ||
+        !encode_output(&tm_dw, dw, n, d, ld_dw, true))
+        return LEMO_ERR_CUDA;
+    const int pairs = wgrad_pairs(dev, sms);
+    if (pairs <= 0) return LEMO_ERR_CUDA;
     wg::Args a = {};
     a.c = view_of(checkpoint);
-    a.dy = dy;
-    a.ld_dy = ld_dy;
-    a.dw = dw;
-    a.ld_dw = ld_dw;
     a.n = n;
     a.d = d;
+    a.tiles_m = (n + wg::TM - 1) / wg::TM;
+    a.tiles_n = (d + wg::TN - 1) / wg::TN;
     a.kept_total = kept_total;
     a.rows = rows;
-    launch(wg::simple_kernel,
-           dim3((unsigned)((d + wg::kTile - 1) / wg::kTile), (unsigned)((n + wg::kTile - 1) / wg::kTile)),
-           256, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        a.spin_limit_ns = (uint64_t)g_spin_ns;
+    }
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    if (tiles > INT_MAX / 2) return LEMO_ERR_UNSUPPORTED;
+    const int use = (int)(tiles < pairs ? tiles : pairs);
+    launch(wg::wgrad_kernel, (unsigned)(2 * use), wg::THREADS, wg::SMEM_BYTES,
+           reinterpret_cast<cudaStream_t>(stream), tm_dy, tm_q, tm_dw, a);
     return launch_status();
 }
 
