@@ -9,24 +9,31 @@
 //
 // Persistent clusters of two CTAs take 256 x 256 output tiles with 2-SM
 // instructions (tcgen05.mma.cta_group::2, M = N = 256, K = 16).  CTA r of a
-// pair holds columns [128 r, +128) of the tile's dy and of its codes.
-//   warp 0     TMA: per 64 rows a 64 x 128 tile of dy (two 128-byte-swizzled
-//              boxes, 16 KB) and the 64 x 128 codes (8 KB) into a ring;
-//   warp 1     (leader) MMA issue into one of two 256-column accumulators;
-//   warps 2-9  per 64 rows: codes -> bf16 B tile in its own ring (64 rows of
-//              128 columns, the MN-major swizzled image), zeroing the rows past
-//              the kept ones in both operands; and, per 1024 rows, read-out of
-//              the finished accumulator.
-// The tensor core's fp32 accumulation truncates: measured against fp64, a sum
-// over K rows of one sign is off by 2.2e-6 at K = 1024 and 3.5e-5 at K = 8192.
-// So an accumulator takes at most 1024 rows; its 128 x 128 values per warp pair are
-// then added (round to nearest) to 128 fp32 registers per thread, while the MMAs
-// fill the other accumulator.
+// pair holds columns [128 r, +128) of the tile's dy and of its codes.  Per stage
+// of 64 kept rows:
+//   warp 0      TMA: a 64 x 128 tile of dy (two 128-byte-swizzled boxes, 16 KB);
+//   warp 3      TMA: the 64 x 128 codes (8 KB), in a ring of their own;
+//   warps 4-19  four teams of four warps, each team every fourth stage: codes ->
+//               bf16 B tile (64 rows of 128 columns, the MN-major swizzled image),
+//               rows past the kept ones zero;
+//   warp 2      passes a landed dy tile on to the leader, after clearing the rows
+//               past the kept ones in the last stage (they may hold anything);
+//   warp 1      (leader) MMA issue into one of two 256-column accumulators.
+// A conversion is five instructions per two values (no table, no fp32 detour);
+// the four teams keep four stages in flight, because one stage's chain (wait,
+// load, convert, store, fence, arrive) takes about twice as long as its MMAs.
+//
+// The tensor core's fp32 accumulation truncates: measured against fp64, sums
+// over K rows are off by 1.0e-6 (random signs) and 2.2e-6 (one sign) at K = 1024,
+// 2.1e-6 and 5.6e-6 at K = 2048, 9.1e-6 and 3.5e-5 at K = 8192.  So an accumulator
+// takes at most 2048 rows; the workers then add it into dW with TMA reduce-adds
+// (fp32, round to nearest, done at L2), while the MMAs fill the other one.  The
+// adds of one tile are issued by one CTA pair, each batch after the one before
+// has completed, so their order and the result are fixed.
 //
 // Every wait is bounded in time; a wait that runs out records LEMO_ERR_TIMEOUT
 // and makes both CTAs of the pair drain what they issued, free their tensor
-// memory and return.  One TMA reduce-add per output element and call, so the
-// result does not depend on timing.
+// memory and return.
 #pragma once
 
 #include <cuda.h>
@@ -41,15 +48,14 @@ namespace wgrad {
 
 using gemm::bulk_commit;
 using gemm::bulk_wait_all;
-using gemm::bulk_wait_read1;
 using gemm::sdesc;
 using gemm::stage_row;
 using gemm::tma_reduce_add_2d;
 using gemm::umma_pair;
-using score::add_f32x2;
 using score::cluster_sync;
 using score::cta_rank;
 using score::map_to_rank;
+using score::mbar_arrive;
 using score::mbar_arrive_cluster;
 using score::mbar_arrive_expect_tx;
 using score::mbar_init;
@@ -64,36 +70,44 @@ using score::umma_commit_pair;
 constexpr int TM = 256, TN = 256;   // output tile of a pair
 constexpr int HALF = 128;           // columns of each operand held by one CTA
 constexpr int KB = 64;              // kept rows per stage
-constexpr int CHUNK = 16;           // stages per accumulator: 1024 rows
-constexpr int IN_STAGES = 4;        // dy tile + codes
-constexpr int B_STAGES = 3;         // bf16 tiles made from codes
+constexpr int CHUNK = 32;           // stages per accumulator: 2048 rows
+constexpr int STAGES = 4;           // dy tiles and bf16 tiles in flight
+constexpr int Q_STAGES = 4;         // code tiles in flight
 constexpr int A_BYTES = KB * HALF * 2;
-constexpr int Q_BYTES = KB * HALF;
-constexpr int IN_BYTES = A_BYTES + Q_BYTES;
 constexpr int B_BYTES = KB * HALF * 2;
-constexpr int WORKERS = 8;          // warps that make B tiles and read accumulators
-constexpr int THREADS = 32 * (2 + WORKERS);
-constexpr int ROWS_PER_WORKER = KB / WORKERS;
-constexpr int STG_BYTES = 32 * 128;
-constexpr int STG_PER_WARP = 2 * STG_BYTES;
+constexpr int Q_BYTES = KB * HALF;
+constexpr int TEAMS = 4;            // teams of workers that take alternate stages
+constexpr int TEAM = 4;             // warps per team: one per TMEM lane quadrant
+constexpr int WORKERS = TEAMS * TEAM;
+constexpr int FIRST_WORKER = 4;
+constexpr int THREADS = 32 * (FIRST_WORKER + WORKERS);
+constexpr int ROWS_PER_WORKER = KB / TEAM;
+constexpr int STEPS = ROWS_PER_WORKER / 4;  // a warp takes 4 rows at a time
+constexpr int COLS_PER_WORKER = TN / TEAMS; // of an accumulator
+constexpr int STG_BYTES = 32 * 128;         // a worker's box of 32 rows x 32 columns
 constexpr int TMEM_COLS = 512;
 
 struct Smem {
-    uint64_t full[IN_STAGES];    // each CTA: its dy tile and codes of a stage landed
-    uint64_t ready[B_STAGES];    // leader: both CTAs' workers finished a stage's operands
-    uint64_t used[IN_STAGES];    // each CTA: the pair's MMAs of a stage completed
+    uint64_t a_full[STAGES];     // each CTA: its dy tile landed
+    uint64_t a_ready[STAGES];    // leader: both CTAs' dy tiles landed (and were cleared)
+    uint64_t b_ready[STAGES];    // leader: both CTAs' bf16 tiles are written
+    uint64_t used[STAGES];       // each CTA: the pair's MMAs of a stage completed
+    uint64_t q_full[Q_STAGES];   // each CTA: its codes landed
+    uint64_t q_empty[Q_STAGES];  // each CTA: a team has read the codes
     uint64_t acc_full[2];        // each CTA: accumulator holds a finished chunk
     uint64_t acc_empty[2];       // leader: both CTAs' workers read an accumulator
     uint64_t done;               // each CTA: every MMA of the leader completed
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr int OFF_B = IN_STAGES * IN_BYTES;
-constexpr int OFF_STG = OFF_B + B_STAGES * B_BYTES;
-constexpr int OFF_BAR = OFF_STG + WORKERS * STG_PER_WARP;
+constexpr int OFF_B = STAGES * A_BYTES;
+constexpr int OFF_Q = OFF_B + STAGES * B_BYTES;
+constexpr int OFF_STG = OFF_Q + Q_STAGES * Q_BYTES;
+constexpr int OFF_BAR = OFF_STG + WORKERS * STG_BYTES;
 constexpr int SMEM_BYTES = OFF_BAR + (int)sizeof(Smem) + 1024 /*align slack*/;
 static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB of shared memory per CTA");
-static_assert(IN_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && Q_BYTES % 1024 == 0 &&
+              STG_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 
 struct Args {
     ckpt::View c;
@@ -157,48 +171,41 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// Four codes to four bf16 values (two words), exactly.
-// e4m3: the code's exponent and mantissa bits moved to bits 4..10 of a bf16
-//   read as value x 2^-120 (subnormal codes as subnormal bf16), so
-//   x 2^120 x 2^(code - 127) follows, in two factors whose exponents fit.
-// int8: magnitude m and sign s: (s 128 + s m) - s 128 is exact, then x 2^(code - 127).
-struct Scale {
-    uint32_t f1, f2;
-};
-
-__device__ __forceinline__ Scale make_scale(uint32_t code, int format) {
-    Scale s;
-    if (format == ckpt::kE4M3) {
-        const uint32_t e = code + 120u;  // exponent field of 2^(code - 7)
-        const uint32_t e1 = e < 254u ? e : 254u;
-        s.f1 = e1 << 7;
-        s.f2 = (127u + e - e1) << 7;
-    } else {
-        s.f1 = code << 7;
-        s.f2 = 0u;
-    }
-    if (code == 255u) s.f1 = 0x7fffu;
-    s.f1 |= s.f1 << 16;
-    s.f2 |= s.f2 << 16;
-    return s;
-}
-
-__device__ __forceinline__ void to_bf16x4(uint32_t q, Scale s, int format, uint32_t& lo,
+// Four codes to four bf16 values (two words), exactly, with the group's scale
+// 2^k as a pair of equal bf16 factors.
+// e4m3: the code's exponent and mantissa bits moved to bits 4..10 of a bf16 read
+//   as value x 2^-120 (subnormal codes as subnormal bf16), so the factor is
+//   2^(k + 120).
+// int8: with the code's low 7 bits l and sign bit s, (128 + l) - (128 + 128 s) is
+//   the value; both terms are a bf16 128 with bits of the code or'ed in, and the
+//   difference is exact.
+__device__ __forceinline__ void to_bf16x4(uint32_t q, uint32_t f, int format, uint32_t& lo,
                                           uint32_t& hi) {
     if (format == ckpt::kE4M3) {
         const uint32_t a = __byte_perm(q, 0u, 0x1404), b = __byte_perm(q, 0u, 0x3424);
-        lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-        hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-        lo = mul_bf16x2(mul_bf16x2(lo, s.f1), s.f2);
-        hi = mul_bf16x2(mul_bf16x2(hi, s.f1), s.f2);
+        lo = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), f);
+        hi = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), f);
     } else {
-        const uint32_t neg = (q >> 7) & 0x01010101u;
-        const uint32_t mag = (q ^ (neg * 255u)) + neg;  // bytes stay below 128: no carries
-        const uint32_t sa = (__byte_perm(q, 0u, 0x1404) & 0x80008000u) | 0x43004300u;
-        const uint32_t sb = (__byte_perm(q, 0u, 0x3424) & 0x80008000u) | 0x43004300u;
-        lo = mul_bf16x2(sub_bf16x2(sa | __byte_perm(mag, 0u, 0x4140), sa), s.f1);
-        hi = mul_bf16x2(sub_bf16x2(sb | __byte_perm(mag, 0u, 0x4342), sb), s.f1);
+        const uint32_t a = __byte_perm(q, 0u, 0x4140), b = __byte_perm(q, 0u, 0x4342);
+        lo = mul_bf16x2(sub_bf16x2((a & 0x007f007fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u), f);
+        hi = mul_bf16x2(sub_bf16x2((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u), f);
     }
+}
+
+// Scale bytes up to this one have a bf16 factor in both formats (2^(134 - 7) is
+// bf16's largest power of two); larger ones, and the NaN marker, take two factors.
+constexpr uint32_t kOneFactor = 134;
+
+__device__ __forceinline__ uint32_t factor(uint32_t code, int format) {
+    // exponent fields code + 120 (e4m3) or code (int8) in both halves
+    return code * 0x00800080u + (format == ckpt::kE4M3 ? 0x3c003c00u : 0u);
+}
+
+__device__ __forceinline__ uint32_t second_factor(uint32_t code, int format, uint32_t& f) {
+    const uint32_t e = format == ckpt::kE4M3 ? code + 120u : code;
+    const uint32_t e1 = e < 254u ? e : 254u;
+    f = e1 * 0x00800080u;
+    return code == 255u ? 0x7fff7fffu : (127u + e - e1) * 0x00800080u;
 }
 
 // Instruction descriptor: D fp32, A and B bf16, both MN-major, M = 256, N = 256.
@@ -226,11 +233,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint64_t lim = a.spin_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < IN_STAGES; ++s) {
-            mbar_init(&sm->full[s], 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sm->a_full[s], 1);
+            mbar_init(&sm->a_ready[s], 2);
+            mbar_init(&sm->b_ready[s], 2 * TEAM);
             mbar_init(&sm->used[s], 1);
         }
-        for (int s = 0; s < B_STAGES; ++s) mbar_init(&sm->ready[s], 2 * WORKERS);
+        for (int s = 0; s < Q_STAGES; ++s) {
+            mbar_init(&sm->q_full[s], 1);
+            mbar_init(&sm->q_empty[s], TEAM);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm->acc_full[b], 1);
             mbar_init(&sm->acc_empty[b], 2 * WORKERS);
@@ -250,32 +262,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = sm->tmem_base;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ TMA producers
         if (lane == 0) {
+            uint64_t* full = warp == 0 ? sm->a_full : sm->q_full;
+            uint64_t* empty = warp == 0 ? sm->used : sm->q_empty;
+            constexpr uint32_t N = STAGES;
+            static_assert(STAGES == Q_STAGES, "one ring index for both producers");
             uint32_t it = 0;
             bool ok = true;
             for (int t = pair; ok && t < total; t += npairs) {
                 const int n0 = (t % a.tiles_m) * TM + (int)rank * HALF;
                 const int c0 = (t / a.tiles_m) * TN + (int)rank * HALF;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const uint32_t s = it % IN_STAGES, ph = (it / IN_STAGES) & 1;
-                    if (!(ok = wait(&sm->used[s], ph ^ 1, sm, lim))) break;
-                    mbar_arrive_expect_tx(&sm->full[s], IN_BYTES);
-                    const uint32_t sa = sbase + s * IN_BYTES;
-                    tma_load(sa, &tm_dy, n0, kb * KB, &sm->full[s]);
-                    tma_load(sa + A_BYTES / 2, &tm_dy, n0 + 64, kb * KB, &sm->full[s]);
-                    tma_load(sa + A_BYTES, &tm_q, c0, kb * KB, &sm->full[s]);
+                    const uint32_t s = it % N, ph = (it / N) & 1;
+                    if (!(ok = wait(&empty[s], ph ^ 1, sm, lim))) break;
+                    if (warp == 0) {
+                        const uint32_t sa = sbase + s * A_BYTES;
+                        mbar_arrive_expect_tx(&full[s], A_BYTES);
+                        tma_load(sa, &tm_dy, n0, kb * KB, &full[s]);
+                        tma_load(sa + A_BYTES / 2, &tm_dy, n0 + 64, kb * KB, &full[s]);
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], Q_BYTES);
+                        tma_load(sbase + OFF_Q + s * Q_BYTES, &tm_q, c0, kb * KB, &full[s]);
+                    }
                 }
             }
             if (!ok) {  // every load in flight lands before the CTA leaves
-                const uint32_t first = it > IN_STAGES ? it - IN_STAGES : 0;
+                const uint32_t first = it > N ? it - N : 0;
                 for (uint32_t j = first; j < it; ++j) {
                     const uint64_t t0 = globaltimer_ns();
-                    while (!mbar_try_wait(&sm->full[j % IN_STAGES], (j / IN_STAGES) & 1) &&
-                           globaltimer_ns() - t0 < lim) {
+                    while (!mbar_try_wait(&full[j % N], (j / N) & 1) && globaltimer_ns() - t0 < lim) {
                     }
                 }
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ dy tiles for the leader
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->a_ready[0]), 0);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < total; t += npairs) {
+            for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                const uint32_t s = it % STAGES;
+                if (!(ok = wait_warp(&sm->a_full[s], (it / STAGES) & 1, sm, lim))) break;
+                const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
+                if (valid < KB) {
+                    // a row is 16 vectors: 8 in each 64-column half
+                    for (int v = valid * 16 + lane; v < KB * 16; v += 32) {
+                        const int row = v >> 4;
+                        *reinterpret_cast<uint4*>(base + s * A_BYTES + ((v >> 3) & 1) * (A_BYTES / 2) +
+                                                  row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
             }
         }
     } else if (warp == 1) {
@@ -284,22 +326,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             uint32_t it = 0, ci = 0;
             bool ok = true;
             for (int t = pair; ok && t < total; t += npairs) {
-                for (int kb = 0; ok && kb < kblocks; ++kb, ++it) {
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const int in_chunk = kb % CHUNK;
-                    const uint32_t buf = ci & 1;
+                    const uint32_t buf = ci & 1, s = it % STAGES, ph = (it / STAGES) & 1;
                     if (in_chunk == 0 &&
                         !(ok = wait(&sm->acc_empty[buf], ((ci >> 1) & 1) ^ 1, sm, lim)))
                         break;
-                    if (!(ok = wait(&sm->ready[it % B_STAGES], (it / B_STAGES) & 1, sm, lim))) break;
+                    if (!(ok = wait(&sm->a_ready[s], ph, sm, lim))) break;
+                    if (!(ok = wait(&sm->b_ready[s], ph, sm, lim))) break;
                     tc_fence_after();
-                    const uint32_t sa = sbase + (it % IN_STAGES) * IN_BYTES;
-                    const uint32_t sb = sbase + OFF_B + (it % B_STAGES) * B_BYTES;
+                    const uint32_t sa = sbase + s * A_BYTES, sb = sbase + OFF_B + s * B_BYTES;
 #pragma unroll
                     for (int k = 0; k < KB / 16; ++k)
                         umma_pair(tmem_base + buf * TN, sdesc(sa + k * 2048, A_BYTES / 2),
                                   sdesc(sb + k * 2048, B_BYTES / 2), kIdesc,
                                   (in_chunk > 0 || k > 0) ? 1u : 0u);
-                    umma_commit_pair(&sm->used[it % IN_STAGES]);
+                    umma_commit_pair(&sm->used[s]);
                     if (in_chunk == CHUNK - 1 || kb == kblocks - 1) {
                         umma_commit_pair(&sm->acc_full[buf]);
                         ++ci;
@@ -320,143 +362,130 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else {
         // ------------------------------------------------------------ workers
-        const int w = warp - 2;
-        const int q = warp & 3, colhalf = w >> 2;  // TMEM lane quadrant, half of the columns
-        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + colhalf * HALF;
-        const uint32_t my_stg = sbase + OFF_STG + w * STG_PER_WARP;
-        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), 0);
+        const int w = warp - FIRST_WORKER;
+        const int team = w / TEAM, q = w % TEAM;  // q: TMEM lane quadrant (= warp % 4)
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + team * COLS_PER_WORKER;
+        const uint32_t my_stg = sbase + OFF_STG + w * STG_BYTES;
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->b_ready[0]), 0);
         const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), 0);
         const int format = a.c.format;
-        // a lane turns 16 columns (chunk) of rows row0 and row0 + 4 of every stage
-        const int row0 = w * ROWS_PER_WORKER + (lane >> 3), chunk = lane & 7;
-        float acc[HALF];
+        // A lane turns 16 columns (chunk) of four rows of a stage.  Lanes of the two 64-column
+        // halves take neighbouring rows, whose swizzles differ in the lowest bit, so that the
+        // 16-byte stores of a quarter warp fall into 8 different bank groups.
+        const int chunk = lane & 7, h = chunk >> 2;
+        const int row0 = q * ROWS_PER_WORKER + ((lane >> 3) ^ h);  // + 4 j: rows of step j
+        const int q_off = row0 * HALF + 16 * chunk;
+        int b_off[2][2];  // [step parity][vector]: bytes inside the B tile
 #pragma unroll
-        for (int i = 0; i < HALF; ++i) acc[i] = 0.f;
-        uint32_t it = 0, ci = 0, nst = 0;  // stages, chunks read, staged boxes
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                b_off[j][e] = h * (B_BYTES / 2) + (row0 + 4 * j) * 128 +
+                              (((2 * (chunk & 3) + e) ^ ((row0 + 4 * j) & 7)) << 4);
+        uint32_t it = 0, ci = 0;  // stages, chunks read
         bool ok = true;
-        int pending = 0;                   // chunks whose MMAs were fed but not read yet
-        bool pending_last = false;
-        int out_n = 0, out_c = 0;          // output of the tile being read
+        bool pending = false;     // a chunk was fed and not read yet
+        int out_n = 0, out_c = 0; // its output
 
-        // Reads the oldest pending accumulator; writes the tile out after its last one.
+        // Reads the oldest accumulator and adds it into dW.
         auto read_chunk = [&]() -> bool {
             const uint32_t buf = ci & 1;
             if (!wait_warp(&sm->acc_full[buf], (ci >> 1) & 1, sm, lim)) return false;
             tc_fence_after();
             const uint32_t tb = lane_addr + buf * TN;
 #pragma unroll
-            for (int ch = 0; ch < HALF; ch += 16) {
-                uint32_t r[16];
+            for (int ch = 0; ch < COLS_PER_WORKER; ch += 32) {
+                uint32_t r[32];
                 tmem_ld16(tb + ch, &r[0]);
+                tmem_ld16(tb + ch + 16, &r[16]);
                 tmem_wait_ld();
-                if (ch + 16 == HALF) {
+                if (ch + 32 == COLS_PER_WORKER) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(empty_c + buf * 8);
                 }
-#pragma unroll
-                for (int i = 0; i < 16; i += 2)
-                    add_f32x2(acc[ch + i], acc[ch + i + 1], __uint_as_float(r[i]),
-                              __uint_as_float(r[i + 1]));
-            }
-            ++ci;
-            --pending;
-            if (!pending_last) return true;
-#pragma unroll
-            for (int ch = 0; ch < HALF; ch += 32) {
-                const int col = out_c + ch;
-                const uint32_t sb = my_stg + (nst & 1) * STG_BYTES;
-                if (lane == 0 && nst >= 2) bulk_wait_read1();
+                // adds issued before have completed: the staging box is free, and the adds of
+                // one element keep their order
+                if (lane == 0) bulk_wait_all();
                 __syncwarp();
-                uint32_t r[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    r[i] = __float_as_uint(acc[ch + i]);
-                    acc[ch + i] = 0.f;
-                }
-                stage_row(sb, lane, r);
+                stage_row(my_stg, lane, r);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    if (col < a.d && out_n < a.n) tma_reduce_add_2d(&tm_dw, sb, col, out_n);
+                    if (out_c + ch < a.d && out_n < a.n)
+                        tma_reduce_add_2d(&tm_dw, my_stg, out_c + ch, out_n);
                     bulk_commit();
                 }
-                ++nst;
             }
+            ++ci;
+            pending = false;
             return true;
         };
 
         for (int t = pair; ok && t < total; t += npairs) {
-            const int tn0 = (t % a.tiles_m) * TM, tc0 = (t / a.tiles_m) * TN;
-            const int grp = (tc0 + (int)rank * HALF) / ckpt::kGroup + (chunk >> 1);
-            const bool has_grp = tc0 + (int)rank * HALF + 16 * chunk < a.d;
-            const uint8_t* scol = a.c.scales + (has_grp ? grp : 0);
+            const int n0 = (t % a.tiles_m) * TM, c0 = (t / a.tiles_m) * TN;
+            const int col = c0 + (int)rank * HALF + 16 * chunk;
+            const bool in = col < a.d;
+            const uint8_t* scol = a.c.scales + (in ? col / ckpt::kGroup : 0);
             auto load_codes = [&](int kb, uint32_t* c) {
+                const int64_t r = (int64_t)kb * KB + row0;
+                const uint8_t* p = scol + r * a.c.ld_scales;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int64_t r = (int64_t)kb * KB + row0 + 4 * j;
-                    c[j] = r < K && has_grp ? __ldg(scol + r * a.c.ld_scales) : 3u;
-                }
+                for (int j = 0; j < STEPS; ++j)
+                    c[j] = in && r + 4 * j < K ? __ldg(p + 4 * j * a.c.ld_scales) : 3u;
             };
-            uint32_t codes[2][2];  // scale bytes of the next two stages
-            load_codes(0, codes[0]);
-            load_codes(1, codes[1]);
+            uint32_t codes[STEPS];  // scale bytes of the team's next stage
+            load_codes((int)((team + TEAMS - it % TEAMS) % TEAMS), codes);
             for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                const uint32_t s = it % IN_STAGES, b = it % B_STAGES;
-                if (!(ok = wait_warp(&sm->full[s], (it / IN_STAGES) & 1, sm, lim))) break;
-                // the MMAs of stage it - B_STAGES have read this B slot
-                if (it >= B_STAGES) {
-                    const uint32_t u = it - B_STAGES;
-                    if (!(ok = wait_warp(&sm->used[u % IN_STAGES], (u / IN_STAGES) & 1, sm, lim)))
-                        break;
-                }
-                const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
-                uint8_t* in = base + s * IN_BYTES;
-                uint8_t* bt = base + OFF_B + b * B_BYTES;
+                if (it % TEAMS == team) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+                    if (!(ok = wait_warp(&sm->q_full[s], ph, sm, lim))) break;
+                    // the MMAs of stage it - STAGES have read this B slot
+                    if (!(ok = wait_warp(&sm->used[s], ph ^ 1, sm, lim))) break;
+                    const uint8_t* qt = base + OFF_Q + s * Q_BYTES + q_off;
+                    uint8_t* bt = base + OFF_B + s * B_BYTES;
+                    uint32_t most = 0;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = row0 + 4 * j;
-                    const uint4 v = *reinterpret_cast<const uint4*>(in + A_BYTES + row * HALF + 16 * chunk);
-                    const Scale sc = make_scale(codes[0][j], format);
-                    uint4 o[2];
-                    to_bf16x4(v.x, sc, format, o[0].x, o[0].y);
-                    to_bf16x4(v.y, sc, format, o[0].z, o[0].w);
-                    to_bf16x4(v.z, sc, format, o[1].x, o[1].y);
-                    to_bf16x4(v.w, sc, format, o[1].z, o[1].w);
-                    if (row >= valid) {
-                        o[0] = o[1] = make_uint4(0u, 0u, 0u, 0u);
-                        // this row of dy: 8 lanes clear its 16 vectors
-                        uint8_t* ar = in + (row >> 3) * 1024 + (row & 7) * 128 + 16 * chunk;
-                        *reinterpret_cast<uint4*>(ar) = o[0];
-                        *reinterpret_cast<uint4*>(ar + A_BYTES / 2) = o[0];
-                    }
-                    // 16-byte vectors 2 (chunk % 4) and + 1 of the row's 64-column half; the two
-                    // halves store them in opposite order, so a quarter warp hits 8 banks groups
-                    const int h = chunk >> 2;
-                    uint8_t* br = bt + h * (B_BYTES / 2) + (row >> 3) * 1024 + (row & 7) * 128;
+                    for (int j = 0; j < STEPS; ++j) most = max(most, codes[j]);
+                    const bool one = !__any_sync(0xffffffffu, most > kOneFactor);
+                    const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int half = e ^ h;
-                        *reinterpret_cast<uint4*>(br + (((2 * (chunk & 3) + half) ^ (row & 7)) << 4)) =
-                            half ? o[1] : o[0];
+                    for (int j = 0; j < STEPS; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(qt + 4 * j * HALF);
+                        uint32_t f = factor(codes[j], format), f2 = 0u;
+                        if (!one) f2 = second_factor(codes[j], format, f);
+                        uint4 o0, o1;
+                        to_bf16x4(v.x, f, format, o0.x, o0.y);
+                        to_bf16x4(v.y, f, format, o0.z, o0.w);
+                        to_bf16x4(v.z, f, format, o1.x, o1.y);
+                        to_bf16x4(v.w, f, format, o1.z, o1.w);
+                        if (!one) {
+                            o0 = make_uint4(mul_bf16x2(o0.x, f2), mul_bf16x2(o0.y, f2),
+                                            mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
+                            o1 = make_uint4(mul_bf16x2(o1.x, f2), mul_bf16x2(o1.y, f2),
+                                            mul_bf16x2(o1.z, f2), mul_bf16x2(o1.w, f2));
+                        }
+                        if (row0 + 4 * j >= valid) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
+                        const int up = (j >> 1) * 8 * 128;
+                        *reinterpret_cast<uint4*>(bt + b_off[j & 1][0] + up) = o0;
+                        *reinterpret_cast<uint4*>(bt + b_off[j & 1][1] + up) = o1;
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_cluster(ready_c + s * 8);
+                        mbar_arrive(&sm->q_empty[s]);
+                    }
+                    load_codes(kb + TEAMS, codes);
                 }
-                codes[0][0] = codes[1][0];
-                codes[0][1] = codes[1][1];
-                load_codes(kb + 2, codes[1]);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ready_c + b * 8);
-                // Once a few stages of this chunk are fed, the chunk before is (nearly) done.
-                if (pending && (kb % CHUNK == B_STAGES || kb == kblocks - 1 ||
-                                kb % CHUNK == CHUNK - 1)) {
+                // Once this chunk's first stages are fed, the chunk before is (nearly) done.
+                if (pending && (kb % CHUNK == STAGES || kb == kblocks - 1 || kb % CHUNK == CHUNK - 1)) {
                     if (!(ok = read_chunk())) break;
                 }
                 if (kb % CHUNK == CHUNK - 1 || kb == kblocks - 1) {
-                    pending = 1;
-                    pending_last = kb == kblocks - 1;
-                    out_n = tn0 + (int)rank * HALF + q * 32;
-                    out_c = tc0 + colhalf * HALF;
+                    pending = true;
+                    out_n = n0 + (int)rank * HALF + q * 32;
+                    out_c = c0 + team * COLS_PER_WORKER;
                 }
             }
         }
