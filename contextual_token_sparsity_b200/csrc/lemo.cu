@@ -1248,14 +1248,31 @@ bool encode_codes(CUtensorMap* tm, const lemo_checkpoint* c) {
            CUDA_SUCCESS;
 }
 
-// CTA pairs of the weight-gradient kernel that fit at once.
-int g_wgrad_pairs[kMaxDevices];
+// 2-D tensor map of the fp32 weight gradient [n, d], boxes of 32 rows x 64
+// bytes with 64-byte swizzle, for the workers' reduce-adds.
+bool encode_wgrad(CUtensorMap* tm, float* dw, int64_t n, int64_t d, int64_t ld) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)n};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * 4)};
+    const cuuint32_t box[2] = {(cuuint32_t)lemo::wgrad::BOX, 32u};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dw, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
 
-int wgrad_pairs(int dev, int sms) {
+// CTA pairs of the weight-gradient kernel of a format that fit at once.
+int g_wgrad_pairs[kMaxDevices][2];
+
+template <typename Kernel>
+int wgrad_pairs(int dev, int sms, int format, Kernel kernel) {
     namespace wg = lemo::wgrad;
     std::lock_guard<std::mutex> lk(g_mu);
-    if (g_wgrad_pairs[dev] == 0) {
-        if (cudaFuncSetAttribute(wg::wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    int& pairs = g_wgrad_pairs[dev][format];
+    if (pairs == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  wg::SMEM_BYTES) != cudaSuccess)
             return 0;
         cudaLaunchConfig_t cfg = {};
@@ -1270,14 +1287,13 @@ int wgrad_pairs(int dev, int sms) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, wg::wgrad_kernel, &cfg) != cudaSuccess ||
-            clusters < 1) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
             cudaGetLastError();
             clusters = sms / 2;
         }
-        g_wgrad_pairs[dev] = clusters < sms / 2 ? clusters : sms / 2;
+        pairs = clusters < sms / 2 ? clusters : sms / 2;
     }
-    return g_wgrad_pairs[dev];
+    return pairs;
 }
 
 // Persistent grid of the element-wise checkpoint kernels.
@@ -1595,9 +1611,11 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     if (sms <= 0) return LEMO_ERR_CUDA;
     CUtensorMap tm_dy, tm_q, tm_dw;
     if (!encode_operand(&tm_dy, dy, rows, n, ld_dy, true) || !encode_codes(&tm_q, checkpoint) ||
-        !encode_output(&tm_dw, dw, n, d, ld_dw, true))
+        !encode_wgrad(&tm_dw, dw, n, d, ld_dw))
         return LEMO_ERR_CUDA;
-    const int pairs = wgrad_pairs(dev, sms);
+    const auto kernel = checkpoint->format == LEMO_CHECKPOINT_E4M3 ? wg::wgrad_kernel<lemo::ckpt::kE4M3>
+                                                                   : wg::wgrad_kernel<lemo::ckpt::kInt8>;
+    const int pairs = wgrad_pairs(dev, sms, checkpoint->format, kernel);
     if (pairs <= 0) return LEMO_ERR_CUDA;
     wg::Args a = {};
     a.c = view_of(checkpoint);
@@ -1614,7 +1632,7 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (tiles > INT_MAX / 2) return LEMO_ERR_UNSUPPORTED;
     const int use = (int)(tiles < pairs ? tiles : pairs);
-    launch(wg::wgrad_kernel, (unsigned)(2 * use), wg::THREADS, wg::SMEM_BYTES,
+    launch(kernel, (unsigned)(2 * use), wg::THREADS, wg::SMEM_BYTES,
            reinterpret_cast<cudaStream_t>(stream), tm_dy, tm_q, tm_dw, a);
     return launch_status();
 }

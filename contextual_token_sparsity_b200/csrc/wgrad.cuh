@@ -39,6 +39,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "ckpt.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
@@ -49,7 +51,6 @@ namespace wgrad {
 using gemm::bulk_commit;
 using gemm::bulk_wait_all;
 using gemm::sdesc;
-using gemm::stage_row;
 using gemm::tma_reduce_add_2d;
 using gemm::umma_pair;
 using score::cluster_sync;
@@ -71,27 +72,30 @@ constexpr int TM = 256, TN = 256;   // output tile of a pair
 constexpr int HALF = 128;           // columns of each operand held by one CTA
 constexpr int KB = 64;              // kept rows per stage
 constexpr int CHUNK = 32;           // stages per accumulator: 2048 rows
-constexpr int STAGES = 4;           // dy tiles and bf16 tiles in flight
+constexpr int A_STAGES = 6;         // dy tiles in flight
+constexpr int B_STAGES = 4;         // bf16 tiles in flight
 constexpr int Q_STAGES = 4;         // code tiles in flight
 constexpr int A_BYTES = KB * HALF * 2;
 constexpr int B_BYTES = KB * HALF * 2;
 constexpr int Q_BYTES = KB * HALF;
 constexpr int TEAMS = 4;            // teams of workers that take alternate stages
 constexpr int TEAM = 4;             // warps per team: one per TMEM lane quadrant
+static_assert(Q_STAGES == TEAMS && B_STAGES == TEAMS, "a team owns one slot of each");
 constexpr int WORKERS = TEAMS * TEAM;
 constexpr int FIRST_WORKER = 4;
 constexpr int THREADS = 32 * (FIRST_WORKER + WORKERS);
 constexpr int ROWS_PER_WORKER = KB / TEAM;
 constexpr int STEPS = ROWS_PER_WORKER / 4;  // a warp takes 4 rows at a time
 constexpr int COLS_PER_WORKER = TN / TEAMS; // of an accumulator
-constexpr int STG_BYTES = 32 * 128;         // a worker's box of 32 rows x 32 columns
+constexpr int BOX = 16;                     // columns of a worker's output box (32 rows)
+constexpr int STG_BYTES = 32 * BOX * 4;
 constexpr int TMEM_COLS = 512;
 
 struct Smem {
-    uint64_t a_full[STAGES];     // each CTA: its dy tile landed
-    uint64_t a_ready[STAGES];    // leader: both CTAs' dy tiles landed (and were cleared)
-    uint64_t b_ready[STAGES];    // leader: both CTAs' bf16 tiles are written
-    uint64_t used[STAGES];       // each CTA: the pair's MMAs of a stage completed
+    uint64_t a_full[A_STAGES];   // each CTA: its dy tile landed
+    uint64_t a_ready[A_STAGES];  // leader: both CTAs' dy tiles landed (and were cleared)
+    uint64_t b_ready[B_STAGES];  // leader: both CTAs' bf16 tiles are written
+    uint64_t used[A_STAGES];     // each CTA: the pair's MMAs of a stage completed
     uint64_t q_full[Q_STAGES];   // each CTA: its codes landed
     uint64_t q_empty[Q_STAGES];  // each CTA: a team has read the codes
     uint64_t acc_full[2];        // each CTA: accumulator holds a finished chunk
@@ -100,8 +104,8 @@ struct Smem {
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr int OFF_B = STAGES * A_BYTES;
-constexpr int OFF_Q = OFF_B + STAGES * B_BYTES;
+constexpr int OFF_B = A_STAGES * A_BYTES;
+constexpr int OFF_Q = OFF_B + B_STAGES * B_BYTES;
 constexpr int OFF_STG = OFF_Q + Q_STAGES * Q_BYTES;
 constexpr int OFF_BAR = OFF_STG + WORKERS * STG_BYTES;
 constexpr int SMEM_BYTES = OFF_BAR + (int)sizeof(Smem) + 1024 /*align slack*/;
@@ -160,6 +164,10 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, in
         : "memory");
 }
 
+__device__ __forceinline__ void bulk_wait_read0() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -179,9 +187,9 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // int8: with the code's low 7 bits l and sign bit s, (128 + l) - (128 + 128 s) is
 //   the value; both terms are a bf16 128 with bits of the code or'ed in, and the
 //   difference is exact.
-__device__ __forceinline__ void to_bf16x4(uint32_t q, uint32_t f, int format, uint32_t& lo,
-                                          uint32_t& hi) {
-    if (format == ckpt::kE4M3) {
+template <int FORMAT>
+__device__ __forceinline__ void to_bf16x4(uint32_t q, uint32_t f, uint32_t& lo, uint32_t& hi) {
+    if constexpr (FORMAT == ckpt::kE4M3) {
         const uint32_t a = __byte_perm(q, 0u, 0x1404), b = __byte_perm(q, 0u, 0x3424);
         lo = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), f);
         hi = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), f);
@@ -196,13 +204,15 @@ __device__ __forceinline__ void to_bf16x4(uint32_t q, uint32_t f, int format, ui
 // bf16's largest power of two); larger ones, and the NaN marker, take two factors.
 constexpr uint32_t kOneFactor = 134;
 
-__device__ __forceinline__ uint32_t factor(uint32_t code, int format) {
+template <int FORMAT>
+__device__ __forceinline__ uint32_t factor(uint32_t code) {
     // exponent fields code + 120 (e4m3) or code (int8) in both halves
-    return code * 0x00800080u + (format == ckpt::kE4M3 ? 0x3c003c00u : 0u);
+    return code * 0x00800080u + (FORMAT == ckpt::kE4M3 ? 0x3c003c00u : 0u);
 }
 
-__device__ __forceinline__ uint32_t second_factor(uint32_t code, int format, uint32_t& f) {
-    const uint32_t e = format == ckpt::kE4M3 ? code + 120u : code;
+template <int FORMAT>
+__device__ __forceinline__ uint32_t second_factor(uint32_t code, uint32_t& f) {
+    const uint32_t e = FORMAT == ckpt::kE4M3 ? code + 120u : code;
     const uint32_t e1 = e < 254u ? e : 254u;
     f = e1 * 0x00800080u;
     return code == 255u ? 0x7fff7fffu : (127u + e - e1) * 0x00800080u;
@@ -212,6 +222,7 @@ __device__ __forceinline__ uint32_t second_factor(uint32_t code, int format, uin
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                             ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
 
+template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_q,
                  const __grid_constant__ CUtensorMap tm_dw, const Args a) {
@@ -233,12 +244,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint64_t lim = a.spin_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < A_STAGES; ++s) {
             mbar_init(&sm->a_full[s], 1);
             mbar_init(&sm->a_ready[s], 2);
-            mbar_init(&sm->b_ready[s], 2 * TEAM);
             mbar_init(&sm->used[s], 1);
         }
+        for (int s = 0; s < B_STAGES; ++s) mbar_init(&sm->b_ready[s], 2 * TEAM);
         for (int s = 0; s < Q_STAGES; ++s) {
             mbar_init(&sm->q_full[s], 1);
             mbar_init(&sm->q_empty[s], TEAM);
@@ -267,15 +278,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             uint64_t* full = warp == 0 ? sm->a_full : sm->q_full;
             uint64_t* empty = warp == 0 ? sm->used : sm->q_empty;
-            constexpr uint32_t N = STAGES;
-            static_assert(STAGES == Q_STAGES, "one ring index for both producers");
-            uint32_t it = 0;
+            const uint32_t N = warp == 0 ? A_STAGES : Q_STAGES;
+            uint32_t it = 0, s = 0, ph = 0;  // stage, its slot and the slot's phase
             bool ok = true;
             for (int t = pair; ok && t < total; t += npairs) {
                 const int n0 = (t % a.tiles_m) * TM + (int)rank * HALF;
                 const int c0 = (t / a.tiles_m) * TN + (int)rank * HALF;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const uint32_t s = it % N, ph = (it / N) & 1;
                     if (!(ok = wait(&empty[s], ph ^ 1, sm, lim))) break;
                     if (warp == 0) {
                         const uint32_t sa = sbase + s * A_BYTES;
@@ -285,6 +294,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     } else {
                         mbar_arrive_expect_tx(&full[s], Q_BYTES);
                         tma_load(sbase + OFF_Q + s * Q_BYTES, &tm_q, c0, kb * KB, &full[s]);
+                    }
+                    if (++s == N) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
             }
@@ -300,12 +313,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ dy tiles for the leader
         const uint32_t ready_c = map_to_rank(smem_u32(&sm->a_ready[0]), 0);
-        uint32_t it = 0;
+        uint32_t s = 0, ph = 0;
         bool ok = true;
         for (int t = pair; ok && t < total; t += npairs) {
-            for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                const uint32_t s = it % STAGES;
-                if (!(ok = wait_warp(&sm->a_full[s], (it / STAGES) & 1, sm, lim))) break;
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!(ok = wait_warp(&sm->a_full[s], ph, sm, lim))) break;
                 const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
                 if (valid < KB) {
                     // a row is 16 vectors: 8 in each 64-column half
@@ -318,24 +330,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
+                if (++s == A_STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0 && leader) {
-            uint32_t it = 0, ci = 0;
+            uint32_t it = 0, ci = 0, s = 0, ph = 0;
             bool ok = true;
             for (int t = pair; ok && t < total; t += npairs) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const int in_chunk = kb % CHUNK;
-                    const uint32_t buf = ci & 1, s = it % STAGES, ph = (it / STAGES) & 1;
+                    const uint32_t buf = ci & 1, b = it % B_STAGES;
                     if (in_chunk == 0 &&
                         !(ok = wait(&sm->acc_empty[buf], ((ci >> 1) & 1) ^ 1, sm, lim)))
                         break;
                     if (!(ok = wait(&sm->a_ready[s], ph, sm, lim))) break;
-                    if (!(ok = wait(&sm->b_ready[s], ph, sm, lim))) break;
+                    if (!(ok = wait(&sm->b_ready[b], (it / B_STAGES) & 1, sm, lim))) break;
                     tc_fence_after();
-                    const uint32_t sa = sbase + s * A_BYTES, sb = sbase + OFF_B + s * B_BYTES;
+                    const uint32_t sa = sbase + s * A_BYTES, sb = sbase + OFF_B + b * B_BYTES;
 #pragma unroll
                     for (int k = 0; k < KB / 16; ++k)
                         umma_pair(tmem_base + buf * TN, sdesc(sa + k * 2048, A_BYTES / 2),
@@ -345,6 +361,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (in_chunk == CHUNK - 1 || kb == kblocks - 1) {
                         umma_commit_pair(&sm->acc_full[buf]);
                         ++ci;
+                    }
+                    if (++s == A_STAGES) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
             }
@@ -368,7 +388,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t my_stg = sbase + OFF_STG + w * STG_BYTES;
         const uint32_t ready_c = map_to_rank(smem_u32(&sm->b_ready[0]), 0);
         const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), 0);
-        const int format = a.c.format;
         // A lane turns 16 columns (chunk) of four rows of a stage.  Lanes of the two 64-column
         // halves take neighbouring rows, whose swizzles differ in the lowest bit, so that the
         // 16-byte stores of a quarter warp fall into 8 different bank groups.
@@ -382,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 2; ++e)
                 b_off[j][e] = h * (B_BYTES / 2) + (row0 + 4 * j) * 128 +
                               (((2 * (chunk & 3) + e) ^ ((row0 + 4 * j) & 7)) << 4);
-        uint32_t it = 0, ci = 0;  // stages, chunks read
+        uint32_t it = 0, ci = 0;  // stages before this tile, chunks read
         bool ok = true;
         bool pending = false;     // a chunk was fed and not read yet
         int out_n = 0, out_c = 0; // its output
@@ -394,21 +413,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tc_fence_after();
             const uint32_t tb = lane_addr + buf * TN;
 #pragma unroll
-            for (int ch = 0; ch < COLS_PER_WORKER; ch += 32) {
-                uint32_t r[32];
-                tmem_ld16(tb + ch, &r[0]);
-                tmem_ld16(tb + ch + 16, &r[16]);
+            for (int ch = 0; ch < COLS_PER_WORKER; ch += BOX) {
+                uint32_t r[BOX];
+                tmem_ld16(tb + ch, r);
                 tmem_wait_ld();
-                if (ch + 32 == COLS_PER_WORKER) {
+                if (ch + BOX == COLS_PER_WORKER) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(empty_c + buf * 8);
                 }
-                // adds issued before have completed: the staging box is free, and the adds of
-                // one element keep their order
-                if (lane == 0) bulk_wait_all();
+                // The chunk before: its adds have completed, so the adds of one element keep
+                // their order.  Between the boxes of this one: the staging box was read.
+                if (lane == 0) {
+                    if (ch == 0) bulk_wait_all();
+                    else bulk_wait_read0();
+                }
                 __syncwarp();
-                stage_row(my_stg, lane, r);
+                const uint32_t row = my_stg + (uint32_t)lane * (BOX * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // 64-byte swizzle: vector j of row l at j ^ (l / 2 % 4)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     row + ((j ^ ((lane >> 1) & 3)) << 4)),
+                                 "r"(r[4 * j]), "r"(r[4 * j + 1]), "r"(r[4 * j + 2]),
+                                 "r"(r[4 * j + 3])
+                                 : "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
@@ -422,72 +450,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             return true;
         };
 
+        // Converts this warp's rows of a stage.  `one`: one factor per scale is enough;
+        // `valid`: rows of the stage that are kept.
+        auto convert = [&](auto one, int valid, const uint8_t* qt, uint8_t* bt, const uint32_t* codes) {
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(qt + 4 * j * HALF);
+                uint32_t f = factor<FORMAT>(codes[j]), f2 = 0u;
+                if constexpr (!one.value) f2 = second_factor<FORMAT>(codes[j], f);
+                uint4 o0, o1;
+                to_bf16x4<FORMAT>(v.x, f, o0.x, o0.y);
+                to_bf16x4<FORMAT>(v.y, f, o0.z, o0.w);
+                to_bf16x4<FORMAT>(v.z, f, o1.x, o1.y);
+                to_bf16x4<FORMAT>(v.w, f, o1.z, o1.w);
+                if constexpr (!one.value) {
+                    o0 = make_uint4(mul_bf16x2(o0.x, f2), mul_bf16x2(o0.y, f2),
+                                    mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
+                    o1 = make_uint4(mul_bf16x2(o1.x, f2), mul_bf16x2(o1.y, f2),
+                                    mul_bf16x2(o1.z, f2), mul_bf16x2(o1.w, f2));
+                    if (row0 + 4 * j >= valid) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
+                }
+                const int up = (j >> 1) * 8 * 128;
+                *reinterpret_cast<uint4*>(bt + b_off[j & 1][0] + up) = o0;
+                *reinterpret_cast<uint4*>(bt + b_off[j & 1][1] + up) = o1;
+            }
+        };
+
+        const int64_t step_scales = 4 * a.c.ld_scales;              // four rows
+        const int64_t turn_scales = (int64_t)TEAMS * KB * a.c.ld_scales;
+        uint32_t turn = 0;        // stages this team has taken: stage = team + TEAMS turn
+        uint32_t us = (uint32_t)team, used_ph = 0;  // dy slot (and its phase) of the stage before
         for (int t = pair; ok && t < total; t += npairs) {
             const int n0 = (t % a.tiles_m) * TM, c0 = (t / a.tiles_m) * TN;
             const int col = c0 + (int)rank * HALF + 16 * chunk;
             const bool in = col < a.d;
-            const uint8_t* scol = a.c.scales + (in ? col / ckpt::kGroup : 0);
-            auto load_codes = [&](int kb, uint32_t* c) {
-                const int64_t r = (int64_t)kb * KB + row0;
-                const uint8_t* p = scol + r * a.c.ld_scales;
+            int kb = (int)((team + TEAMS - it % TEAMS) % TEAMS);    // this team's next stage
+            const uint8_t* sp = a.c.scales + (in ? col / ckpt::kGroup : 0) +
+                                ((int64_t)kb * KB + row0) * a.c.ld_scales;
+            auto load_codes = [&](uint32_t* c) {
+                const int left = in ? (int)min(K - (int64_t)kb * KB - row0, (int64_t)KB) : 0;
 #pragma unroll
-                for (int j = 0; j < STEPS; ++j)
-                    c[j] = in && r + 4 * j < K ? __ldg(p + 4 * j * a.c.ld_scales) : 3u;
+                for (int j = 0; j < STEPS; ++j) c[j] = 4 * j < left ? __ldg(sp + j * step_scales) : 3u;
             };
             uint32_t codes[STEPS];  // scale bytes of the team's next stage
-            load_codes((int)((team + TEAMS - it % TEAMS) % TEAMS), codes);
-            for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                if (it % TEAMS == team) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
-                    if (!(ok = wait_warp(&sm->q_full[s], ph, sm, lim))) break;
-                    // the MMAs of stage it - STAGES have read this B slot
-                    if (!(ok = wait_warp(&sm->used[s], ph ^ 1, sm, lim))) break;
+            load_codes(codes);
+            for (int c_end = 0; ok && c_end < kblocks;) {
+                // the stages of one accumulator: [c_end - CHUNK, c_end)
+                c_end = min(c_end + CHUNK, kblocks);
+                const int c_begin = (c_end - 1) / CHUNK * CHUNK;
+                while (kb < c_end) {
+                    const uint32_t s = (uint32_t)team;  // this team's slot of codes and bf16 tile
+                    if (!(ok = wait_warp(&sm->q_full[s], turn & 1, sm, lim))) break;
+                    // the MMAs of this team's stage before have read the slot
+                    if (turn > 0 && !(ok = wait_warp(&sm->used[us], used_ph, sm, lim))) break;
                     const uint8_t* qt = base + OFF_Q + s * Q_BYTES + q_off;
                     uint8_t* bt = base + OFF_B + s * B_BYTES;
                     uint32_t most = 0;
 #pragma unroll
                     for (int j = 0; j < STEPS; ++j) most = max(most, codes[j]);
-                    const bool one = !__any_sync(0xffffffffu, most > kOneFactor);
                     const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
-#pragma unroll
-                    for (int j = 0; j < STEPS; ++j) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(qt + 4 * j * HALF);
-                        uint32_t f = factor(codes[j], format), f2 = 0u;
-                        if (!one) f2 = second_factor(codes[j], format, f);
-                        uint4 o0, o1;
-                        to_bf16x4(v.x, f, format, o0.x, o0.y);
-                        to_bf16x4(v.y, f, format, o0.z, o0.w);
-                        to_bf16x4(v.z, f, format, o1.x, o1.y);
-                        to_bf16x4(v.w, f, format, o1.z, o1.w);
-                        if (!one) {
-                            o0 = make_uint4(mul_bf16x2(o0.x, f2), mul_bf16x2(o0.y, f2),
-                                            mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
-                            o1 = make_uint4(mul_bf16x2(o1.x, f2), mul_bf16x2(o1.y, f2),
-                                            mul_bf16x2(o1.z, f2), mul_bf16x2(o1.w, f2));
-                        }
-                        if (row0 + 4 * j >= valid) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
-                        const int up = (j >> 1) * 8 * 128;
-                        *reinterpret_cast<uint4*>(bt + b_off[j & 1][0] + up) = o0;
-                        *reinterpret_cast<uint4*>(bt + b_off[j & 1][1] + up) = o1;
-                    }
+                    if (valid == KB && !__any_sync(0xffffffffu, most > kOneFactor))
+                        convert(std::true_type{}, valid, qt, bt, codes);
+                    else
+                        convert(std::false_type{}, valid, qt, bt, codes);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive_cluster(ready_c + s * 8);
                         mbar_arrive(&sm->q_empty[s]);
                     }
-                    load_codes(kb + TEAMS, codes);
+                    kb += TEAMS;
+                    sp += turn_scales;
+                    load_codes(codes);
+                    if (turn > 0) {  // one turn on
+                        us += TEAMS;
+                        if (us >= A_STAGES) {
+                            us -= A_STAGES;
+                            used_ph ^= 1;
+                        }
+                    }
+                    ++turn;
+                    // Once this chunk's first stages were used, the chunk before is done.
+                    if (pending && kb - TEAMS >= c_begin + B_STAGES && !(ok = read_chunk())) break;
                 }
-                // Once this chunk's first stages are fed, the chunk before is (nearly) done.
-                if (pending && (kb % CHUNK == STAGES || kb == kblocks - 1 || kb % CHUNK == CHUNK - 1)) {
-                    if (!(ok = read_chunk())) break;
-                }
-                if (kb % CHUNK == CHUNK - 1 || kb == kblocks - 1) {
-                    pending = true;
-                    out_n = n0 + (int)rank * HALF + q * 32;
-                    out_c = c0 + team * COLS_PER_WORKER;
-                }
+                if (ok && pending) ok = read_chunk();
+                pending = true;
+                out_n = n0 + (int)rank * HALF + q * 32;
+                out_c = c0 + team * COLS_PER_WORKER;
             }
+            it += (uint32_t)kblocks;
         }
         if (ok && pending) read_chunk();
         if (lane == 0) bulk_wait_all();  // every reduce-add landed before the CTA exits
