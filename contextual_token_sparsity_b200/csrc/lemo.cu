@@ -1248,21 +1248,6 @@ bool encode_codes(CUtensorMap* tm, const lemo_checkpoint* c) {
            CUDA_SUCCESS;
 }
 
-// 2-D tensor map of the fp32 weight gradient [n, d], boxes of 32 rows x 64
-// bytes with 64-byte swizzle, for the workers' reduce-adds.
-bool encode_wgrad(CUtensorMap* tm, float* dw, int64_t n, int64_t d, int64_t ld) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)n};
-    const cuuint64_t strides[1] = {(cuuint64_t)(ld * 4)};
-    const cuuint32_t box[2] = {(cuuint32_t)lemo::wgrad::BOX, 32u};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dw, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
-
 // CTA pairs of the weight-gradient kernel of a format that fit at once.
 int g_wgrad_pairs[kMaxDevices][2];
 
@@ -1601,7 +1586,7 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     if (e != LEMO_OK) return e;
     if ((e = check_checkpoint(checkpoint, d, rows)) != LEMO_OK) return e;
     if (n < 1) return LEMO_ERR_INVALID_ARG;
-    if (n % 8 != 0) return LEMO_ERR_UNSUPPORTED;
+    if (n % 8 != 0 || rows > (1 << 30)) return LEMO_ERR_UNSUPPORTED;
     if (!mat_ok(dy, ld_dy, n) || !dw || !aligned(dw, 16) || ld_dw < d || ld_dw % 4 != 0)
         return LEMO_ERR_INVALID_ARG;
     if (rows == 0) return LEMO_OK;
@@ -1611,7 +1596,7 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     if (sms <= 0) return LEMO_ERR_CUDA;
     CUtensorMap tm_dy, tm_q, tm_dw;
     if (!encode_operand(&tm_dy, dy, rows, n, ld_dy, true) || !encode_codes(&tm_q, checkpoint) ||
-        !encode_wgrad(&tm_dw, dw, n, d, ld_dw))
+        !encode_output(&tm_dw, dw, n, d, ld_dw, true))
         return LEMO_ERR_CUDA;
     const auto kernel = checkpoint->format == LEMO_CHECKPOINT_E4M3 ? wg::wgrad_kernel<lemo::ckpt::kE4M3>
                                                                    : wg::wgrad_kernel<lemo::ckpt::kInt8>;

@@ -18,7 +18,8 @@
 //               rows past the kept ones zero;
 //   warp 2      passes a landed dy tile on to the leader, after clearing the rows
 //               past the kept ones in the last stage (they may hold anything);
-//   warp 1      (leader) MMA issue into one of two 256-column accumulators.
+//   warp 1      (leader) MMA issue into one of two 256-column accumulators;
+//   warps 20-23 read-out of a finished accumulator, one TMEM lane quadrant each.
 // A conversion is five instructions per two values (no table, no fp32 detour);
 // the four teams keep four stages in flight, because one stage's chain (wait,
 // load, convert, store, fence, arrive) takes about twice as long as its MMAs.
@@ -26,10 +27,10 @@
 // The tensor core's fp32 accumulation truncates: measured against fp64, sums
 // over K rows are off by 1.0e-6 (random signs) and 2.2e-6 (one sign) at K = 1024,
 // 2.1e-6 and 5.6e-6 at K = 2048, 9.1e-6 and 3.5e-5 at K = 8192.  So an accumulator
-// takes at most 2048 rows; the workers then add it into dW with TMA reduce-adds
-// (fp32, round to nearest, done at L2), while the MMAs fill the other one.  The
-// adds of one tile are issued by one CTA pair, each batch after the one before
-// has completed, so their order and the result are fixed.
+// takes at most 2048 rows and is then added into dW with TMA reduce-adds (fp32,
+// round to nearest, done at L2), while the MMAs fill the other one.  The adds of
+// one tile are issued by one CTA pair, each accumulator's after those of the one
+// before have completed, so their order and the result are fixed.
 //
 // Every wait is bounded in time; a wait that runs out records LEMO_ERR_TIMEOUT
 // and makes both CTAs of the pair drain what they issued, free their tensor
@@ -50,7 +51,9 @@ namespace wgrad {
 
 using gemm::bulk_commit;
 using gemm::bulk_wait_all;
+using gemm::bulk_wait_read1;
 using gemm::sdesc;
+using gemm::stage_row;
 using gemm::tma_reduce_add_2d;
 using gemm::umma_pair;
 using score::cluster_sync;
@@ -83,23 +86,23 @@ constexpr int TEAM = 4;             // warps per team: one per TMEM lane quadran
 static_assert(Q_STAGES == TEAMS && B_STAGES == TEAMS, "a team owns one slot of each");
 constexpr int WORKERS = TEAMS * TEAM;
 constexpr int FIRST_WORKER = 4;
-constexpr int THREADS = 32 * (FIRST_WORKER + WORKERS);
+constexpr int FIRST_READER = FIRST_WORKER + WORKERS;
+constexpr int READERS = 4;          // warps that read accumulators: one per lane quadrant
+constexpr int THREADS = 32 * (FIRST_READER + READERS);
 constexpr int ROWS_PER_WORKER = KB / TEAM;
 constexpr int STEPS = ROWS_PER_WORKER / 4;  // a warp takes 4 rows at a time
-constexpr int COLS_PER_WORKER = TN / TEAMS; // of an accumulator
-constexpr int BOX = 16;                     // columns of a worker's output box (32 rows)
+constexpr int BOX = 32;             // columns of an output box (32 rows, 128 bytes each)
 constexpr int STG_BYTES = 32 * BOX * 4;
 constexpr int TMEM_COLS = 512;
 
 struct Smem {
     uint64_t a_full[A_STAGES];   // each CTA: its dy tile landed
-    uint64_t a_ready[A_STAGES];  // leader: both CTAs' dy tiles landed (and were cleared)
-    uint64_t b_ready[B_STAGES];  // leader: both CTAs' bf16 tiles are written
+    uint64_t ready[B_STAGES];    // leader: both CTAs' dy and bf16 tiles are in place
     uint64_t used[A_STAGES];     // each CTA: the pair's MMAs of a stage completed
     uint64_t q_full[Q_STAGES];   // each CTA: its codes landed
     uint64_t q_empty[Q_STAGES];  // each CTA: a team has read the codes
     uint64_t acc_full[2];        // each CTA: accumulator holds a finished chunk
-    uint64_t acc_empty[2];       // leader: both CTAs' workers read an accumulator
+    uint64_t acc_empty[2];       // leader: both CTAs' readers read an accumulator
     uint64_t done;               // each CTA: every MMA of the leader completed
     uint32_t tmem_base;
     int abort_flag;
@@ -107,7 +110,7 @@ struct Smem {
 constexpr int OFF_B = A_STAGES * A_BYTES;
 constexpr int OFF_Q = OFF_B + B_STAGES * B_BYTES;
 constexpr int OFF_STG = OFF_Q + Q_STAGES * Q_BYTES;
-constexpr int OFF_BAR = OFF_STG + WORKERS * STG_BYTES;
+constexpr int OFF_BAR = OFF_STG + READERS * 2 * STG_BYTES;
 constexpr int SMEM_BYTES = OFF_BAR + (int)sizeof(Smem) + 1024 /*align slack*/;
 static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB of shared memory per CTA");
 static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && Q_BYTES % 1024 == 0 &&
@@ -162,10 +165,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, in
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
-}
-
-__device__ __forceinline__ void bulk_wait_read0() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -246,17 +245,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < A_STAGES; ++s) {
             mbar_init(&sm->a_full[s], 1);
-            mbar_init(&sm->a_ready[s], 2);
             mbar_init(&sm->used[s], 1);
         }
-        for (int s = 0; s < B_STAGES; ++s) mbar_init(&sm->b_ready[s], 2 * TEAM);
+        for (int s = 0; s < B_STAGES; ++s) mbar_init(&sm->ready[s], 2 * (TEAM + 1));
         for (int s = 0; s < Q_STAGES; ++s) {
             mbar_init(&sm->q_full[s], 1);
             mbar_init(&sm->q_empty[s], TEAM);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm->acc_full[b], 1);
-            mbar_init(&sm->acc_empty[b], 2 * WORKERS);
+            mbar_init(&sm->acc_empty[b], 2 * READERS);
         }
         mbar_init(&sm->done, 1);
         sm->abort_flag = 0;
@@ -312,12 +310,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ dy tiles for the leader
-        const uint32_t ready_c = map_to_rank(smem_u32(&sm->a_ready[0]), 0);
-        uint32_t s = 0, ph = 0;
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), 0);
+        uint32_t it = 0, s = 0, ph = 0, us = 0, used_ph = 0;
         bool ok = true;
         for (int t = pair; ok && t < total; t += npairs) {
-            for (int kb = 0; kb < kblocks; ++kb) {
+            for (int kb = 0; kb < kblocks; ++kb, ++it) {
                 if (!(ok = wait_warp(&sm->a_full[s], ph, sm, lim))) break;
+                // `ready` turns over with the bf16 slots: not before stage it - B_STAGES was used
+                if (it >= B_STAGES) {
+                    if (!(ok = wait_warp(&sm->used[us], used_ph, sm, lim))) break;
+                    if (++us == A_STAGES) {
+                        us = 0;
+                        used_ph ^= 1;
+                    }
+                }
                 const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
                 if (valid < KB) {
                     // a row is 16 vectors: 8 in each 64-column half
@@ -329,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
+                if (lane == 0) mbar_arrive_cluster(ready_c + (it % B_STAGES) * 8);
                 if (++s == A_STAGES) {
                     s = 0;
                     ph ^= 1;
@@ -339,33 +345,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0 && leader) {
-            uint32_t it = 0, ci = 0, s = 0, ph = 0;
+            // descriptors of slot 0; a slot is A_BYTES (B_BYTES) further, a K step 2048 bytes
+            const uint64_t da0 = sdesc(sbase, A_BYTES / 2), db0 = sdesc(sbase + OFF_B, B_BYTES / 2);
+            uint32_t s = 0, b = 0, ready_ph = 0, buf = 0, empty_ph = 1;
             bool ok = true;
             for (int t = pair; ok && t < total; t += npairs) {
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const int in_chunk = kb % CHUNK;
-                    const uint32_t buf = ci & 1, b = it % B_STAGES;
-                    if (in_chunk == 0 &&
-                        !(ok = wait(&sm->acc_empty[buf], ((ci >> 1) & 1) ^ 1, sm, lim)))
-                        break;
-                    if (!(ok = wait(&sm->a_ready[s], ph, sm, lim))) break;
-                    if (!(ok = wait(&sm->b_ready[b], (it / B_STAGES) & 1, sm, lim))) break;
-                    tc_fence_after();
-                    const uint32_t sa = sbase + s * A_BYTES, sb = sbase + OFF_B + b * B_BYTES;
+                for (int k0 = 0; ok && k0 < kblocks; k0 += CHUNK) {
+                    if (!(ok = wait(&sm->acc_empty[buf], empty_ph, sm, lim))) break;
+                    const uint32_t d_tmem = tmem_base + buf * TN;
+                    const int k1 = min(k0 + CHUNK, kblocks);
+                    for (int kb = k0; kb < k1; ++kb) {
+                        const uint64_t da = da0 + s * (A_BYTES >> 4), db = db0 + b * (B_BYTES >> 4);
+                        if (!(ok = wait(&sm->ready[b], ready_ph, sm, lim))) break;
+                        tc_fence_after();
+                        umma_pair(d_tmem, da, db, kIdesc, kb > k0 ? 1u : 0u);
 #pragma unroll
-                    for (int k = 0; k < KB / 16; ++k)
-                        umma_pair(tmem_base + buf * TN, sdesc(sa + k * 2048, A_BYTES / 2),
-                                  sdesc(sb + k * 2048, B_BYTES / 2), kIdesc,
-                                  (in_chunk > 0 || k > 0) ? 1u : 0u);
-                    umma_commit_pair(&sm->used[s]);
-                    if (in_chunk == CHUNK - 1 || kb == kblocks - 1) {
-                        umma_commit_pair(&sm->acc_full[buf]);
-                        ++ci;
+                        for (int k = 1; k < KB / 16; ++k)
+                            umma_pair(d_tmem, da + k * (2048 >> 4), db + k * (2048 >> 4), kIdesc, 1u);
+                        umma_commit_pair(&sm->used[s]);
+                        s = s + 1 == A_STAGES ? 0u : s + 1;
+                        b = (b + 1) % B_STAGES;
+                        ready_ph ^= b == 0 ? 1u : 0u;
                     }
-                    if (++s == A_STAGES) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                    if (!ok) break;
+                    umma_commit_pair(&sm->acc_full[buf]);
+                    buf ^= 1;
+                    empty_ph ^= buf == 0 ? 1u : 0u;
                 }
             }
             umma_commit_pair(&sm->done);
@@ -380,14 +385,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             }
         }
-    } else {
+    } else if (warp < FIRST_READER) {
         // ------------------------------------------------------------ workers
         const int w = warp - FIRST_WORKER;
-        const int team = w / TEAM, q = w % TEAM;  // q: TMEM lane quadrant (= warp % 4)
-        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16) + team * COLS_PER_WORKER;
-        const uint32_t my_stg = sbase + OFF_STG + w * STG_BYTES;
-        const uint32_t ready_c = map_to_rank(smem_u32(&sm->b_ready[0]), 0);
-        const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), 0);
+        const int team = w / TEAM, q = w % TEAM;
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[team]), 0);
         // A lane turns 16 columns (chunk) of four rows of a stage.  Lanes of the two 64-column
         // halves take neighbouring rows, whose swizzles differ in the lowest bit, so that the
         // 16-byte stores of a quarter warp fall into 8 different bank groups.
@@ -401,58 +403,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 2; ++e)
                 b_off[j][e] = h * (B_BYTES / 2) + (row0 + 4 * j) * 128 +
                               (((2 * (chunk & 3) + e) ^ ((row0 + 4 * j) & 7)) << 4);
-        uint32_t it = 0, ci = 0;  // stages before this tile, chunks read
-        bool ok = true;
-        bool pending = false;     // a chunk was fed and not read yet
-        int out_n = 0, out_c = 0; // its output
-
-        // Reads the oldest accumulator and adds it into dW.
-        auto read_chunk = [&]() -> bool {
-            const uint32_t buf = ci & 1;
-            if (!wait_warp(&sm->acc_full[buf], (ci >> 1) & 1, sm, lim)) return false;
-            tc_fence_after();
-            const uint32_t tb = lane_addr + buf * TN;
-#pragma unroll
-            for (int ch = 0; ch < COLS_PER_WORKER; ch += BOX) {
-                uint32_t r[BOX];
-                tmem_ld16(tb + ch, r);
-                tmem_wait_ld();
-                if (ch + BOX == COLS_PER_WORKER) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(empty_c + buf * 8);
-                }
-                // The chunk before: its adds have completed, so the adds of one element keep
-                // their order.  Between the boxes of this one: the staging box was read.
-                if (lane == 0) {
-                    if (ch == 0) bulk_wait_all();
-                    else bulk_wait_read0();
-                }
-                __syncwarp();
-                const uint32_t row = my_stg + (uint32_t)lane * (BOX * 4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)  // 64-byte swizzle: vector j of row l at j ^ (l / 2 % 4)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     row + ((j ^ ((lane >> 1) & 3)) << 4)),
-                                 "r"(r[4 * j]), "r"(r[4 * j + 1]), "r"(r[4 * j + 2]),
-                                 "r"(r[4 * j + 3])
-                                 : "memory");
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    if (out_c + ch < a.d && out_n < a.n)
-                        tma_reduce_add_2d(&tm_dw, my_stg, out_c + ch, out_n);
-                    bulk_commit();
-                }
-            }
-            ++ci;
-            pending = false;
-            return true;
-        };
-
-        // Converts this warp's rows of a stage.  `one`: one factor per scale is enough;
-        // `valid`: rows of the stage that are kept.
-        auto convert = [&](auto one, int valid, const uint8_t* qt, uint8_t* bt, const uint32_t* codes) {
+        const int64_t step_scales = 4 * a.c.ld_scales;              // four rows
+        const int64_t turn_scales = (int64_t)TEAMS * KB * a.c.ld_scales;
+        const int full_blocks = (int)(K / KB);
+        const uint8_t* const qt = base + OFF_Q + team * Q_BYTES + q_off;  // the team's own slots
+        uint8_t* const bt = base + OFF_B + team * B_BYTES;
+        // Converts this warp's rows of a stage.  `one`: one factor per scale is enough and every
+        // row is kept; otherwise the lane's rows from `left` on are zero.
+        auto convert = [&](auto one, int left, const uint32_t* codes) {
 #pragma unroll
             for (int j = 0; j < STEPS; ++j) {
                 const uint4 v = *reinterpret_cast<const uint4*>(qt + 4 * j * HALF);
@@ -468,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                     mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
                     o1 = make_uint4(mul_bf16x2(o1.x, f2), mul_bf16x2(o1.y, f2),
                                     mul_bf16x2(o1.z, f2), mul_bf16x2(o1.w, f2));
-                    if (row0 + 4 * j >= valid) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
+                    if (4 * j >= left) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
                 }
                 const int up = (j >> 1) * 8 * 128;
                 *reinterpret_cast<uint4*>(bt + b_off[j & 1][0] + up) = o0;
@@ -476,71 +434,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
         };
 
-        const int64_t step_scales = 4 * a.c.ld_scales;              // four rows
-        const int64_t turn_scales = (int64_t)TEAMS * KB * a.c.ld_scales;
         uint32_t turn = 0;        // stages this team has taken: stage = team + TEAMS turn
         uint32_t us = (uint32_t)team, used_ph = 0;  // dy slot (and its phase) of the stage before
-        for (int t = pair; ok && t < total; t += npairs) {
-            const int n0 = (t % a.tiles_m) * TM, c0 = (t / a.tiles_m) * TN;
+        uint32_t it = 0;          // stages before this tile
+        bool ok = true;
+        for (int t = pair; ok && t < total; t += npairs, it += (uint32_t)kblocks) {
+            const int c0 = (t / a.tiles_m) * TN;
             const int col = c0 + (int)rank * HALF + 16 * chunk;
             const bool in = col < a.d;
             int kb = (int)((team + TEAMS - it % TEAMS) % TEAMS);    // this team's next stage
             const uint8_t* sp = a.c.scales + (in ? col / ckpt::kGroup : 0) +
                                 ((int64_t)kb * KB + row0) * a.c.ld_scales;
-            auto load_codes = [&](uint32_t* c) {
-                const int left = in ? (int)min(K - (int64_t)kb * KB - row0, (int64_t)KB) : 0;
-#pragma unroll
-                for (int j = 0; j < STEPS; ++j) c[j] = 4 * j < left ? __ldg(sp + j * step_scales) : 3u;
-            };
+            int left = (int)K - kb * KB - row0;  // rows from this lane's first
             uint32_t codes[STEPS];  // scale bytes of the team's next stage
-            load_codes(codes);
-            for (int c_end = 0; ok && c_end < kblocks;) {
-                // the stages of one accumulator: [c_end - CHUNK, c_end)
-                c_end = min(c_end + CHUNK, kblocks);
-                const int c_begin = (c_end - 1) / CHUNK * CHUNK;
-                while (kb < c_end) {
-                    const uint32_t s = (uint32_t)team;  // this team's slot of codes and bf16 tile
-                    if (!(ok = wait_warp(&sm->q_full[s], turn & 1, sm, lim))) break;
-                    // the MMAs of this team's stage before have read the slot
-                    if (turn > 0 && !(ok = wait_warp(&sm->used[us], used_ph, sm, lim))) break;
-                    const uint8_t* qt = base + OFF_Q + s * Q_BYTES + q_off;
-                    uint8_t* bt = base + OFF_B + s * B_BYTES;
-                    uint32_t most = 0;
+            auto load_codes = [&]() {
 #pragma unroll
-                    for (int j = 0; j < STEPS; ++j) most = max(most, codes[j]);
-                    const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
-                    if (valid == KB && !__any_sync(0xffffffffu, most > kOneFactor))
-                        convert(std::true_type{}, valid, qt, bt, codes);
-                    else
-                        convert(std::false_type{}, valid, qt, bt, codes);
+                for (int j = 0; j < STEPS; ++j)
+                    codes[j] = in && 4 * j < left ? __ldg(sp + j * step_scales) : 3u;
+            };
+            load_codes();
+            for (; kb < kblocks; kb += TEAMS, ++turn) {
+                if (!(ok = wait_warp(&sm->q_full[team], turn & 1, sm, lim))) break;
+                if (turn > 0) {
+                    // the MMAs of this team's stage before have read the slot
+                    if (!(ok = wait_warp(&sm->used[us], used_ph, sm, lim))) break;
+                    us += TEAMS;
+                    if (us >= A_STAGES) {
+                        us -= A_STAGES;
+                        used_ph ^= 1;
+                    }
+                }
+                uint32_t most = 0;
+#pragma unroll
+                for (int j = 0; j < STEPS; ++j) most = max(most, codes[j]);
+                if (kb < full_blocks && !__any_sync(0xffffffffu, most > kOneFactor))
+                    convert(std::true_type{}, left, codes);
+                else
+                    convert(std::false_type{}, left, codes);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(ready_c);
+                    mbar_arrive(&sm->q_empty[team]);
+                }
+                sp += turn_scales;
+                left -= TEAMS * KB;
+                load_codes();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ accumulator readers
+        const int q = warp & 3;  // TMEM lane quadrant
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
+        const uint32_t my_stg = sbase + OFF_STG + (warp - FIRST_READER) * 2 * STG_BYTES;
+        const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), 0);
+        uint32_t buf = 0, full_ph = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < total; t += npairs) {
+            const int out_n = (t % a.tiles_m) * TM + (int)rank * HALF + q * 32;
+            const int c0 = (t / a.tiles_m) * TN;
+            for (int k0 = 0; k0 < kblocks; k0 += CHUNK) {
+                if (!(ok = wait_warp(&sm->acc_full[buf], full_ph, sm, lim))) break;
+                tc_fence_after();
+                // adds of the accumulator before have completed: one element's adds keep their order
+                if (lane == 0) bulk_wait_all();
+#pragma unroll 1
+                for (int ch = 0; ch < TN; ch += BOX) {
+                    uint32_t r[BOX];
+                    tmem_ld16(lane_addr + buf * TN + ch, &r[0]);
+                    tmem_ld16(lane_addr + buf * TN + ch + 16, &r[16]);
+                    tmem_wait_ld();
+                    if (ch + BOX == TN) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(empty_c + buf * 8);
+                    }
+                    const uint32_t box = my_stg + ((ch / BOX) & 1) * STG_BYTES;
+                    if (lane == 0) bulk_wait_read1();  // the box before last has been read
+                    __syncwarp();
+                    stage_row(box, lane, r);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive_cluster(ready_c + s * 8);
-                        mbar_arrive(&sm->q_empty[s]);
+                        if (c0 + ch < a.d && out_n < a.n)
+                            tma_reduce_add_2d(&tm_dw, box, c0 + ch, out_n);
+                        bulk_commit();
                     }
-                    kb += TEAMS;
-                    sp += turn_scales;
-                    load_codes(codes);
-                    if (turn > 0) {  // one turn on
-                        us += TEAMS;
-                        if (us >= A_STAGES) {
-                            us -= A_STAGES;
-                            used_ph ^= 1;
-                        }
-                    }
-                    ++turn;
-                    // Once this chunk's first stages were used, the chunk before is done.
-                    if (pending && kb - TEAMS >= c_begin + B_STAGES && !(ok = read_chunk())) break;
                 }
-                if (ok && pending) ok = read_chunk();
-                pending = true;
-                out_n = n0 + (int)rank * HALF + q * 32;
-                out_c = c0 + team * COLS_PER_WORKER;
+                buf ^= 1;
+                full_ph ^= buf == 0 ? 1u : 0u;
             }
-            it += (uint32_t)kblocks;
         }
-        if (ok && pending) read_chunk();
         if (lane == 0) bulk_wait_all();  // every reduce-add landed before the CTA exits
         __syncwarp();
     }
