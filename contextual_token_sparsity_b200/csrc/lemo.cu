@@ -1233,21 +1233,6 @@ lemo::norm::Args norm_args(lemo_norm norm, int32_t d, const uint16_t* w, const u
 
 bool eps_ok(float eps) { return eps >= 0.f && eps < __builtin_inff(); }
 
-// 2-D tensor map of a checkpoint's codes [rows, d] (bytes), boxes of 128
-// columns x 64 rows, not swizzled.
-bool encode_codes(CUtensorMap* tm, const lemo_checkpoint* c) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)c->d, (cuuint64_t)c->rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)c->ld_data};
-    const cuuint32_t box[2] = {(cuuint32_t)lemo::wgrad::HALF, (cuuint32_t)lemo::wgrad::KB};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c->data, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
-
 // CTA pairs of the weight-gradient kernel of a format that fit at once.
 int g_wgrad_pairs[kMaxDevices][2];
 
@@ -1594,8 +1579,8 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     int dev = 0;
     const int sms = device_sms(&dev);
     if (sms <= 0) return LEMO_ERR_CUDA;
-    CUtensorMap tm_dy, tm_q, tm_dw;
-    if (!encode_operand(&tm_dy, dy, rows, n, ld_dy, true) || !encode_codes(&tm_q, checkpoint) ||
+    CUtensorMap tm_dy, tm_dw;
+    if (!encode_operand(&tm_dy, dy, rows, n, ld_dy, true) ||
         !encode_output(&tm_dw, dw, n, d, ld_dw, true))
         return LEMO_ERR_CUDA;
     const auto kernel = checkpoint->format == LEMO_CHECKPOINT_E4M3 ? wg::wgrad_kernel<lemo::ckpt::kE4M3>
@@ -1607,18 +1592,20 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     a.n = n;
     a.d = d;
     a.tiles_m = (n + wg::TM - 1) / wg::TM;
-    a.tiles_n = (d + wg::TN - 1) / wg::TN;
     a.kept_total = kept_total;
     a.rows = rows;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         a.spin_limit_ns = (uint64_t)g_spin_ns;
     }
-    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    if (tiles > INT_MAX / 2) return LEMO_ERR_UNSUPPORTED;
-    const int use = (int)(tiles < pairs ? tiles : pairs);
+    const int64_t tiles = (int64_t)a.tiles_m * ((d + wg::TN - 1) / wg::TN);
+    if (tiles > INT_MAX / 4) return LEMO_ERR_UNSUPPORTED;
+    const int64_t rest = tiles % pairs;  // tiles of the last round, in halves if those fit in it
+    a.whole = (int)(2 * rest <= pairs ? tiles - rest : tiles);
+    a.items = (int)(a.whole + 2 * (tiles - a.whole));
+    const int use = a.items < pairs ? a.items : pairs;
     launch(kernel, (unsigned)(2 * use), wg::THREADS, wg::SMEM_BYTES,
-           reinterpret_cast<cudaStream_t>(stream), tm_dy, tm_q, tm_dw, a);
+           reinterpret_cast<cudaStream_t>(stream), tm_dy, tm_dw, a);
     return launch_status();
 }
 

@@ -12,17 +12,18 @@
 // pair holds columns [128 r, +128) of the tile's dy and of its codes.  Per stage
 // of 64 kept rows:
 //   warp 0      TMA: a 64 x 128 tile of dy (two 128-byte-swizzled boxes, 16 KB);
-//   warp 3      TMA: the 64 x 128 codes (8 KB), in a ring of their own;
-//   warps 4-19  four teams of four warps, each team every fourth stage: codes ->
-//               bf16 B tile (64 rows of 128 columns, the MN-major swizzled image),
-//               rows past the kept ones zero;
+//   12 warps    three teams of four warps, each team every third stage: codes
+//               (loaded to registers a turn ahead) -> bf16 B tile (64 rows of
+//               128 columns, the MN-major swizzled image), rows past the kept
+//               ones zero;
 //   warp 2      passes a landed dy tile on to the leader, after clearing the rows
 //               past the kept ones in the last stage (they may hold anything);
 //   warp 1      (leader) MMA issue into one of two 256-column accumulators;
 //   warps 20-23 read-out of a finished accumulator, one TMEM lane quadrant each.
-// A conversion is five instructions per two values (no table, no fp32 detour);
-// the four teams keep four stages in flight, because one stage's chain (wait,
-// load, convert, store, fence, arrive) takes about twice as long as its MMAs.
+// A conversion is five instructions per two values (no table, no fp32 detour).
+// The converting warps sit on three of the SM's four schedulers (warp % 4 != 1):
+// sharing the issuer's scheduler stretched its few instructions between two MMAs
+// and with them every stage, 765 cycles against 613 without conversions.
 //
 // The tensor core's fp32 accumulation truncates: measured against fp64, sums
 // over K rows are off by 1.0e-6 (random signs) and 2.2e-6 (one sign) at K = 1024,
@@ -75,18 +76,14 @@ constexpr int TM = 256, TN = 256;   // output tile of a pair
 constexpr int HALF = 128;           // columns of each operand held by one CTA
 constexpr int KB = 64;              // kept rows per stage
 constexpr int CHUNK = 32;           // stages per accumulator: 2048 rows
-constexpr int A_STAGES = 6;         // dy tiles in flight
-constexpr int B_STAGES = 4;         // bf16 tiles in flight
-constexpr int Q_STAGES = 4;         // code tiles in flight
+constexpr int STAGES = 6;           // dy tiles and bf16 tiles in flight
 constexpr int A_BYTES = KB * HALF * 2;
 constexpr int B_BYTES = KB * HALF * 2;
-constexpr int Q_BYTES = KB * HALF;
-constexpr int TEAMS = 4;            // teams of workers that take alternate stages
-constexpr int TEAM = 4;             // warps per team: one per TMEM lane quadrant
-static_assert(Q_STAGES == TEAMS && B_STAGES == TEAMS, "a team owns one slot of each");
+constexpr int TEAMS = 3;            // teams of workers that take alternate stages
+constexpr int TEAM = 4;             // warps per team
 constexpr int WORKERS = TEAMS * TEAM;
-constexpr int FIRST_WORKER = 4;
-constexpr int FIRST_READER = FIRST_WORKER + WORKERS;
+constexpr int FIRST_WORKER = 4;     // warps 4 .. 19 but those of scheduler 1
+constexpr int FIRST_READER = FIRST_WORKER + WORKERS / 3 * 4;
 constexpr int READERS = 4;          // warps that read accumulators: one per lane quadrant
 constexpr int THREADS = 32 * (FIRST_READER + READERS);
 constexpr int ROWS_PER_WORKER = KB / TEAM;
@@ -96,30 +93,28 @@ constexpr int STG_BYTES = 32 * BOX * 4;
 constexpr int TMEM_COLS = 512;
 
 struct Smem {
-    uint64_t a_full[A_STAGES];   // each CTA: its dy tile landed
-    uint64_t ready[B_STAGES];    // leader: both CTAs' dy and bf16 tiles are in place
-    uint64_t used[A_STAGES];     // each CTA: the pair's MMAs of a stage completed
-    uint64_t q_full[Q_STAGES];   // each CTA: its codes landed
-    uint64_t q_empty[Q_STAGES];  // each CTA: a team has read the codes
+    uint64_t a_full[STAGES];     // each CTA: its dy tile landed
+    uint64_t ready[STAGES];      // leader: both CTAs' dy and bf16 tiles are in place
+    uint64_t used[STAGES];       // each CTA: the pair's MMAs of a stage completed
     uint64_t acc_full[2];        // each CTA: accumulator holds a finished chunk
     uint64_t acc_empty[2];       // leader: both CTAs' readers read an accumulator
     uint64_t done;               // each CTA: every MMA of the leader completed
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr int OFF_B = A_STAGES * A_BYTES;
-constexpr int OFF_Q = OFF_B + B_STAGES * B_BYTES;
-constexpr int OFF_STG = OFF_Q + Q_STAGES * Q_BYTES;
+constexpr int OFF_B = STAGES * A_BYTES;
+constexpr int OFF_STG = OFF_B + STAGES * B_BYTES;
 constexpr int OFF_BAR = OFF_STG + READERS * 2 * STG_BYTES;
 constexpr int SMEM_BYTES = OFF_BAR + (int)sizeof(Smem) + 1024 /*align slack*/;
 static_assert(SMEM_BYTES <= 232448, "exceeds the 227 KB of shared memory per CTA");
-static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && Q_BYTES % 1024 == 0 &&
-              STG_BYTES % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && STG_BYTES % 1024 == 0,
+              "swizzled tiles are 1024-byte aligned");
 
 struct Args {
     ckpt::View c;
     int n, d;
-    int tiles_m, tiles_n;
+    int tiles_m;
+    int whole, items;            // items below `whole` are 256 x 256 tiles, the others 256 x 128 halves
     const int32_t* kept_total;
     int64_t rows;
     uint64_t spin_limit_ns;
@@ -165,6 +160,25 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* tm, in
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
+}
+
+// Whether the phase of the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -217,20 +231,46 @@ __device__ __forceinline__ uint32_t second_factor(uint32_t code, uint32_t& f) {
     return code == 255u ? 0x7fff7fffu : (127u + e - e1) * 0x00800080u;
 }
 
-// Instruction descriptor: D fp32, A and B bf16, both MN-major, M = 256, N = 256.
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                            ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
+// Instruction descriptor: D fp32, A and B bf16, both MN-major, M = 256, N = n.
+__device__ __forceinline__ constexpr uint32_t idesc(int n) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(TM >> 4) << 24);
+}
+
+// One item of a pair: rows [n0, +256), columns [c0, +width) of dW, each CTA
+// converting width / 2 of the columns.  When the last round of tiles would
+// leave at least half of the pairs idle the host cuts its tiles in two
+// (4928 x 4096 x 4096 has 256 tiles for 74 pairs: 3.5 rounds instead of 4), and
+// a tile whose columns end within its first half is one anyway.
+struct Item {
+    int n0, c0, width;  // width 0: nothing there
+};
+
+__device__ __forceinline__ Item item_of(const Args& a, int i) {
+    Item r;
+    int t = i, half = 0;
+    r.width = TN;
+    if (i >= a.whole) {
+        t = a.whole + ((i - a.whole) >> 1);
+        half = (i - a.whole) & 1;
+        r.width = HALF;
+    }
+    r.n0 = (t % a.tiles_m) * TM;
+    r.c0 = (t / a.tiles_m) * TN + half * HALF;
+    if (a.d - r.c0 <= HALF) r.width = HALF;
+    if (r.c0 >= a.d) r.width = 0;
+    return r;
+}
 
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    wgrad_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_q,
-                 const __grid_constant__ CUtensorMap tm_dw, const Args a) {
+    wgrad_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_dw,
+                 const Args a) {
     pdl_entry();
     const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
     const int kblocks = (int)((K + KB - 1) / KB);
-    const int total = a.tiles_m * a.tiles_n;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    if (kblocks == 0 || pair >= total) return;  // both CTAs of the pair leave together
+    if (kblocks == 0 || pair >= a.items) return;  // both CTAs of the pair leave together
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -243,14 +283,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint64_t lim = a.spin_limit_ns;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < A_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm->a_full[s], 1);
+            mbar_init(&sm->ready[s], 2 * (TEAM + 1));
             mbar_init(&sm->used[s], 1);
-        }
-        for (int s = 0; s < B_STAGES; ++s) mbar_init(&sm->ready[s], 2 * (TEAM + 1));
-        for (int s = 0; s < Q_STAGES; ++s) {
-            mbar_init(&sm->q_full[s], 1);
-            mbar_init(&sm->q_empty[s], TEAM);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm->acc_full[b], 1);
@@ -271,39 +307,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = sm->tmem_base;
 
-    if (warp == 0 || warp == 3) {
-        // ------------------------------------------------------------ TMA producers
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
-            uint64_t* full = warp == 0 ? sm->a_full : sm->q_full;
-            uint64_t* empty = warp == 0 ? sm->used : sm->q_empty;
-            const uint32_t N = warp == 0 ? A_STAGES : Q_STAGES;
             uint32_t it = 0, s = 0, ph = 0;  // stage, its slot and the slot's phase
             bool ok = true;
-            for (int t = pair; ok && t < total; t += npairs) {
-                const int n0 = (t % a.tiles_m) * TM + (int)rank * HALF;
-                const int c0 = (t / a.tiles_m) * TN + (int)rank * HALF;
+            for (int i = pair; ok && i < a.items; i += npairs) {
+                const Item im = item_of(a, i);
+                if (im.width == 0) continue;
+                const int n0 = im.n0 + (int)rank * HALF;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    if (!(ok = wait(&empty[s], ph ^ 1, sm, lim))) break;
-                    if (warp == 0) {
-                        const uint32_t sa = sbase + s * A_BYTES;
-                        mbar_arrive_expect_tx(&full[s], A_BYTES);
-                        tma_load(sa, &tm_dy, n0, kb * KB, &full[s]);
-                        tma_load(sa + A_BYTES / 2, &tm_dy, n0 + 64, kb * KB, &full[s]);
-                    } else {
-                        mbar_arrive_expect_tx(&full[s], Q_BYTES);
-                        tma_load(sbase + OFF_Q + s * Q_BYTES, &tm_q, c0, kb * KB, &full[s]);
-                    }
-                    if (++s == N) {
+                    if (!(ok = wait(&sm->used[s], ph ^ 1, sm, lim))) break;
+                    const uint32_t sa = sbase + s * A_BYTES;
+                    mbar_arrive_expect_tx(&sm->a_full[s], A_BYTES);
+                    tma_load(sa, &tm_dy, n0, kb * KB, &sm->a_full[s]);
+                    tma_load(sa + A_BYTES / 2, &tm_dy, n0 + 64, kb * KB, &sm->a_full[s]);
+                    if (++s == STAGES) {
                         s = 0;
                         ph ^= 1;
                     }
                 }
             }
             if (!ok) {  // every load in flight lands before the CTA leaves
-                const uint32_t first = it > N ? it - N : 0;
+                const uint32_t first = it > STAGES ? it - STAGES : 0;
                 for (uint32_t j = first; j < it; ++j) {
                     const uint64_t t0 = globaltimer_ns();
-                    while (!mbar_try_wait(&full[j % N], (j / N) & 1) && globaltimer_ns() - t0 < lim) {
+                    while (!mbar_try_wait(&sm->a_full[j % STAGES], (j / STAGES) & 1) &&
+                           globaltimer_ns() - t0 < lim) {
                     }
                 }
             }
@@ -311,32 +341,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ dy tiles for the leader
         const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), 0);
-        uint32_t it = 0, s = 0, ph = 0, us = 0, used_ph = 0;
+        uint32_t s = 0, ph = 0;
         bool ok = true;
-        for (int t = pair; ok && t < total; t += npairs) {
-            for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        for (int i = pair; ok && i < a.items; i += npairs) {
+            if (item_of(a, i).width == 0) continue;
+            for (int kb = 0; kb < kblocks; ++kb) {
                 if (!(ok = wait_warp(&sm->a_full[s], ph, sm, lim))) break;
-                // `ready` turns over with the bf16 slots: not before stage it - B_STAGES was used
-                if (it >= B_STAGES) {
-                    if (!(ok = wait_warp(&sm->used[us], used_ph, sm, lim))) break;
-                    if (++us == A_STAGES) {
-                        us = 0;
-                        used_ph ^= 1;
-                    }
-                }
                 const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
                 if (valid < KB) {
                     // a row is 16 vectors: 8 in each 64-column half
                     for (int v = valid * 16 + lane; v < KB * 16; v += 32) {
                         const int row = v >> 4;
-                        *reinterpret_cast<uint4*>(base + s * A_BYTES + ((v >> 3) & 1) * (A_BYTES / 2) +
-                                                  row * 128 + (v & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        st_shared(sbase + s * A_BYTES + ((v >> 3) & 1) * (A_BYTES / 2) + row * 128 +
+                                      (v & 7) * 16,
+                                  make_uint4(0u, 0u, 0u, 0u));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_cluster(ready_c + (it % B_STAGES) * 8);
-                if (++s == A_STAGES) {
+                if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
+                if (++s == STAGES) {
                     s = 0;
                     ph ^= 1;
                 }
@@ -347,25 +371,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0 && leader) {
             // descriptors of slot 0; a slot is A_BYTES (B_BYTES) further, a K step 2048 bytes
             const uint64_t da0 = sdesc(sbase, A_BYTES / 2), db0 = sdesc(sbase + OFF_B, B_BYTES / 2);
-            uint32_t s = 0, b = 0, ready_ph = 0, buf = 0, empty_ph = 1;
-            bool ok = true;
-            for (int t = pair; ok && t < total; t += npairs) {
+            // One MMA keeps the pipe busy for ~137 cycles and the pipe queues about two, so what
+            // this thread does between two MMAs has to fit in ~270 cycles: the next stage is
+            // tested for in the middle of this one's MMAs, and waited for only if that failed.
+            uint32_t s = 0, ready_ph = 0, buf = 0, empty_ph = 1;
+            bool ok = true, seen = false;  // seen: `ready` of the stage at hand was observed
+            for (int i = pair; ok && i < a.items; i += npairs) {
+                const Item im = item_of(a, i);
+                if (im.width == 0) continue;
+                const uint32_t id = im.width == TN ? idesc(TN) : idesc(HALF);
                 for (int k0 = 0; ok && k0 < kblocks; k0 += CHUNK) {
                     if (!(ok = wait(&sm->acc_empty[buf], empty_ph, sm, lim))) break;
                     const uint32_t d_tmem = tmem_base + buf * TN;
                     const int k1 = min(k0 + CHUNK, kblocks);
                     for (int kb = k0; kb < k1; ++kb) {
-                        const uint64_t da = da0 + s * (A_BYTES >> 4), db = db0 + b * (B_BYTES >> 4);
-                        if (!(ok = wait(&sm->ready[b], ready_ph, sm, lim))) break;
+                        const uint64_t da = da0 + s * (A_BYTES >> 4), db = db0 + s * (B_BYTES >> 4);
+                        if (!seen && !(ok = wait(&sm->ready[s], ready_ph, sm, lim))) break;
                         tc_fence_after();
-                        umma_pair(d_tmem, da, db, kIdesc, kb > k0 ? 1u : 0u);
-#pragma unroll
-                        for (int k = 1; k < KB / 16; ++k)
-                            umma_pair(d_tmem, da + k * (2048 >> 4), db + k * (2048 >> 4), kIdesc, 1u);
-                        umma_commit_pair(&sm->used[s]);
-                        s = s + 1 == A_STAGES ? 0u : s + 1;
-                        b = (b + 1) % B_STAGES;
-                        ready_ph ^= b == 0 ? 1u : 0u;
+                        umma_pair(d_tmem, da, db, id, kb > k0 ? 1u : 0u);
+                        umma_pair(d_tmem, da + (2048 >> 4), db + (2048 >> 4), id, 1u);
+                        const uint32_t used_now = s;
+                        s = s + 1 == STAGES ? 0u : s + 1;
+                        ready_ph ^= s == 0 ? 1u : 0u;
+                        seen = mbar_test(&sm->ready[s], ready_ph);
+                        umma_pair(d_tmem, da + 2 * (2048 >> 4), db + 2 * (2048 >> 4), id, 1u);
+                        umma_pair(d_tmem, da + 3 * (2048 >> 4), db + 3 * (2048 >> 4), id, 1u);
+                        umma_commit_pair(&sm->used[used_now]);
                     }
                     if (!ok) break;
                     umma_commit_pair(&sm->acc_full[buf]);
@@ -385,104 +416,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             }
         }
-    } else if (warp < FIRST_READER) {
+    } else if (warp >= FIRST_WORKER && warp < FIRST_READER && warp % 4 != 1) {
         // ------------------------------------------------------------ workers
-        const int w = warp - FIRST_WORKER;
+        const int w = (warp - FIRST_WORKER) / 4 * 3 + (warp % 4 ? warp % 4 - 1 : 0);  // 0 .. 11
         const int team = w / TEAM, q = w % TEAM;
-        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[team]), 0);
-        // A lane turns 16 columns (chunk) of four rows of a stage.  Lanes of the two 64-column
-        // halves take neighbouring rows, whose swizzles differ in the lowest bit, so that the
-        // 16-byte stores of a quarter warp fall into 8 different bank groups.
-        const int chunk = lane & 7, h = chunk >> 2;
-        const int row0 = q * ROWS_PER_WORKER + ((lane >> 3) ^ h);  // + 4 j: rows of step j
-        const int q_off = row0 * HALF + 16 * chunk;
-        int b_off[2][2];  // [step parity][vector]: bytes inside the B tile
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                b_off[j][e] = h * (B_BYTES / 2) + (row0 + 4 * j) * 128 +
-                              (((2 * (chunk & 3) + e) ^ ((row0 + 4 * j) & 7)) << 4);
-        const int64_t step_scales = 4 * a.c.ld_scales;              // four rows
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), 0);
         const int64_t turn_scales = (int64_t)TEAMS * KB * a.c.ld_scales;
+        const int64_t turn_data = (int64_t)TEAMS * KB * a.c.ld;
         const int full_blocks = (int)(K / KB);
-        const uint8_t* const qt = base + OFF_Q + team * Q_BYTES + q_off;  // the team's own slots
-        uint8_t* const bt = base + OFF_B + team * B_BYTES;
-        // Converts this warp's rows of a stage.  `one`: one factor per scale is enough and every
-        // row is kept; otherwise the lane's rows from `left` on are zero.
-        auto convert = [&](auto one, int left, const uint32_t* codes) {
-#pragma unroll
-            for (int j = 0; j < STEPS; ++j) {
-                const uint4 v = *reinterpret_cast<const uint4*>(qt + 4 * j * HALF);
-                uint32_t f = factor<FORMAT>(codes[j]), f2 = 0u;
-                if constexpr (!one.value) f2 = second_factor<FORMAT>(codes[j], f);
-                uint4 o0, o1;
-                to_bf16x4<FORMAT>(v.x, f, o0.x, o0.y);
-                to_bf16x4<FORMAT>(v.y, f, o0.z, o0.w);
-                to_bf16x4<FORMAT>(v.z, f, o1.x, o1.y);
-                to_bf16x4<FORMAT>(v.w, f, o1.z, o1.w);
-                if constexpr (!one.value) {
-                    o0 = make_uint4(mul_bf16x2(o0.x, f2), mul_bf16x2(o0.y, f2),
-                                    mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
-                    o1 = make_uint4(mul_bf16x2(o1.x, f2), mul_bf16x2(o1.y, f2),
-                                    mul_bf16x2(o1.z, f2), mul_bf16x2(o1.w, f2));
-                    if (4 * j >= left) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
-                }
-                const int up = (j >> 1) * 8 * 128;
-                *reinterpret_cast<uint4*>(bt + b_off[j & 1][0] + up) = o0;
-                *reinterpret_cast<uint4*>(bt + b_off[j & 1][1] + up) = o1;
-            }
-        };
-
         uint32_t turn = 0;        // stages this team has taken: stage = team + TEAMS turn
-        uint32_t us = (uint32_t)team, used_ph = 0;  // dy slot (and its phase) of the stage before
-        uint32_t it = 0;          // stages before this tile
+        uint32_t it = 0;          // stages before this item
         bool ok = true;
-        for (int t = pair; ok && t < total; t += npairs, it += (uint32_t)kblocks) {
-            const int c0 = (t / a.tiles_m) * TN;
-            const int col = c0 + (int)rank * HALF + 16 * chunk;
+        for (int i = pair; ok && i < a.items; i += npairs) {
+            const Item im = item_of(a, i);
+            if (im.width == 0) continue;
+            const bool wide = im.width == TN;
+            // A lane turns 16 columns (chunk) of 4 rows, 4 apart (wide: 128 columns per CTA), or
+            // of 2 rows, 8 apart (64 columns).  Wide, lanes of the two 64-column halves take
+            // neighbouring rows: their swizzles differ in the lowest bit, so the 16-byte stores
+            // of a quarter warp fall into 8 different bank groups.
+            const int chunk = wide ? lane & 7 : lane & 3, h = chunk >> 2;
+            const int row0 = q * ROWS_PER_WORKER + (wide ? (lane >> 3) ^ h : lane >> 2);
+            const int gap = wide ? 4 : 8;
+            uint32_t b_off[2][2];  // [step parity][vector] (64 columns: steps are 8 rows, one parity)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    b_off[j][e] = h * (B_BYTES / 2) + (row0 + 4 * j) * 128 +
+                                  (((2 * (chunk & 3) + e) ^ ((row0 + 4 * j) & 7)) << 4);
+            // Converts this warp's rows of a stage.  `one`: one factor per scale is enough and
+            // every row is kept; otherwise the lane's rows from `left` on are zero.
+            auto convert = [&](auto wide_c, auto one, uint32_t bt, int left, const uint4* val,
+                               const uint32_t* codes) {
+                constexpr int N = wide_c.value ? STEPS : STEPS / 2, GAP = wide_c.value ? 4 : 8;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const uint4 v = val[j];
+                    uint32_t f = factor<FORMAT>(codes[j]), f2 = 0u;
+                    if constexpr (!one.value) f2 = second_factor<FORMAT>(codes[j], f);
+                    uint4 o0, o1;
+                    to_bf16x4<FORMAT>(v.x, f, o0.x, o0.y);
+                    to_bf16x4<FORMAT>(v.y, f, o0.z, o0.w);
+                    to_bf16x4<FORMAT>(v.z, f, o1.x, o1.y);
+                    to_bf16x4<FORMAT>(v.w, f, o1.z, o1.w);
+                    if constexpr (!one.value) {
+                        o0 = make_uint4(mul_bf16x2(o0.x, f2), mul_bf16x2(o0.y, f2),
+                                        mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
+                        o1 = make_uint4(mul_bf16x2(o1.x, f2), mul_bf16x2(o1.y, f2),
+                                        mul_bf16x2(o1.z, f2), mul_bf16x2(o1.w, f2));
+                        if (GAP * j >= left) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    const int par = wide_c.value ? j & 1 : 0, up = (wide_c.value ? j >> 1 : j) * 8 * 128;
+                    st_shared(bt + b_off[par][0] + up, o0);
+                    st_shared(bt + b_off[par][1] + up, o1);
+                }
+            };
+            const int col = im.c0 + (int)rank * (im.width / 2) + 16 * chunk;
             const bool in = col < a.d;
             int kb = (int)((team + TEAMS - it % TEAMS) % TEAMS);    // this team's next stage
-            const uint8_t* sp = a.c.scales + (in ? col / ckpt::kGroup : 0) +
-                                ((int64_t)kb * KB + row0) * a.c.ld_scales;
+            const int64_t first = (int64_t)kb * KB + row0;
+            const uint8_t* sp = a.c.scales + (in ? col / ckpt::kGroup : 0) + first * a.c.ld_scales;
+            const uint8_t* dp = a.c.data + (in ? col : 0) + first * a.c.ld;
+            const int64_t step_scales = gap * a.c.ld_scales, step_data = gap * a.c.ld;
             int left = (int)K - kb * KB - row0;  // rows from this lane's first
-            uint32_t codes[STEPS];  // scale bytes of the team's next stage
-            auto load_codes = [&]() {
+            uint4 val[STEPS];       // codes and scale bytes of the team's next stage
+            uint32_t codes[STEPS];
+            auto load = [&]() {
 #pragma unroll
-                for (int j = 0; j < STEPS; ++j)
-                    codes[j] = in && 4 * j < left ? __ldg(sp + j * step_scales) : 3u;
-            };
-            load_codes();
-            for (; kb < kblocks; kb += TEAMS, ++turn) {
-                if (!(ok = wait_warp(&sm->q_full[team], turn & 1, sm, lim))) break;
-                if (turn > 0) {
-                    // the MMAs of this team's stage before have read the slot
-                    if (!(ok = wait_warp(&sm->used[us], used_ph, sm, lim))) break;
-                    us += TEAMS;
-                    if (us >= A_STAGES) {
-                        us -= A_STAGES;
-                        used_ph ^= 1;
-                    }
+                for (int j = 0; j < STEPS; ++j) {
+                    const bool on = in && gap * j < left && (wide || j < STEPS / 2);
+                    val[j] = on ? __ldg(reinterpret_cast<const uint4*>(dp + j * step_data)) : make_uint4(0u, 0u, 0u, 0u);
+                    codes[j] = on ? __ldg(sp + j * step_scales) : 3u;
                 }
+            };
+            load();
+            for (; kb < kblocks; kb += TEAMS, ++turn) {
+                // the MMAs of the stage STAGES before have read the slot
+                const uint32_t s = team + (turn & 1) * TEAMS;
+                if (!(ok = wait_warp(&sm->used[s], ((turn >> 1) & 1) ^ 1, sm, lim))) break;
+                const uint32_t bt = sbase + OFF_B + s * B_BYTES;
                 uint32_t most = 0;
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) most = max(most, codes[j]);
-                if (kb < full_blocks && !__any_sync(0xffffffffu, most > kOneFactor))
-                    convert(std::true_type{}, left, codes);
+                const bool one = kb < full_blocks && !__any_sync(0xffffffffu, most > kOneFactor);
+                if (wide && one)
+                    convert(std::true_type{}, std::true_type{}, bt, left, val, codes);
+                else if (wide)
+                    convert(std::true_type{}, std::false_type{}, bt, left, val, codes);
+                else if (one)
+                    convert(std::false_type{}, std::true_type{}, bt, left, val, codes);
                 else
-                    convert(std::false_type{}, left, codes);
+                    convert(std::false_type{}, std::false_type{}, bt, left, val, codes);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_cluster(ready_c);
-                    mbar_arrive(&sm->q_empty[team]);
-                }
+                if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
                 sp += turn_scales;
+                dp += turn_data;
                 left -= TEAMS * KB;
-                load_codes();
+                load();
             }
+            it += (uint32_t)kblocks;
         }
-    } else {
+    } else if (warp >= FIRST_READER) {
         // ------------------------------------------------------------ accumulator readers
         const int q = warp & 3;  // TMEM lane quadrant
         const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -490,21 +526,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), 0);
         uint32_t buf = 0, full_ph = 0;
         bool ok = true;
-        for (int t = pair; ok && t < total; t += npairs) {
-            const int out_n = (t % a.tiles_m) * TM + (int)rank * HALF + q * 32;
-            const int c0 = (t / a.tiles_m) * TN;
+        for (int i = pair; ok && i < a.items; i += npairs) {
+            const Item im = item_of(a, i);
+            if (im.width == 0) continue;
+            const int out_n = im.n0 + (int)rank * HALF + q * 32;
             for (int k0 = 0; k0 < kblocks; k0 += CHUNK) {
                 if (!(ok = wait_warp(&sm->acc_full[buf], full_ph, sm, lim))) break;
                 tc_fence_after();
                 // adds of the accumulator before have completed: one element's adds keep their order
                 if (lane == 0) bulk_wait_all();
 #pragma unroll 1
-                for (int ch = 0; ch < TN; ch += BOX) {
+                for (int ch = 0; ch < im.width; ch += BOX) {
                     uint32_t r[BOX];
                     tmem_ld16(lane_addr + buf * TN + ch, &r[0]);
                     tmem_ld16(lane_addr + buf * TN + ch + 16, &r[16]);
                     tmem_wait_ld();
-                    if (ch + BOX == TN) {
+                    if (ch + BOX == im.width) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(empty_c + buf * 8);
@@ -516,8 +553,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
-                        if (c0 + ch < a.d && out_n < a.n)
-                            tma_reduce_add_2d(&tm_dw, box, c0 + ch, out_n);
+                        if (im.c0 + ch < a.d && out_n < a.n)
+                            tma_reduce_add_2d(&tm_dw, box, im.c0 + ch, out_n);
                         bulk_commit();
                     }
                 }
