@@ -186,30 +186,52 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+// (a & b) | c in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// a + b as a x 1 + b (one instruction of the FMA pipe)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x3f803f80u), "r"(b));
     return d;
 }
 
 // Four codes to four bf16 values (two words), exactly, with the group's scale
-// 2^k as a pair of equal bf16 factors.
+// 2^k as a pair of equal bf16 factors.  The even codes make one word and the odd
+// codes the other, which needs no byte permutation: columns 1 and 2 of every four
+// change places in the B tile, and the readers put them back.
 // e4m3: the code's exponent and mantissa bits moved to bits 4..10 of a bf16 read
 //   as value x 2^-120 (subnormal codes as subnormal bf16), so the factor is
-//   2^(k + 120).
+//   2^(k + 120).  Left shifts are written as products: they then run on the FMA
+//   pipe, the integer pipe being the busiest.
 // int8: with the code's low 7 bits l and sign bit s, (128 + l) - (128 + 128 s) is
-//   the value; both terms are a bf16 128 with bits of the code or'ed in, and the
-//   difference is exact.
+//   the value; both terms are a bf16 +-128 with bits of the code or'ed in, and the
+//   sum is exact.
+
+// bf16 +-128 twice, kept in registers: (x & constant) | constant is one
+// instruction only if one of the two constants is.
+struct Consts {
+    uint32_t plus, minus;
+    __device__ __forceinline__ Consts() {
+        asm volatile("mov.b32 %0, 0x43004300;" : "=r"(plus));
+        asm volatile("mov.b32 %0, 0xc300c300;" : "=r"(minus));
+    }
+};
+
 template <int FORMAT>
-__device__ __forceinline__ void to_bf16x4(uint32_t q, uint32_t f, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void to_bf16x4(uint32_t q, uint32_t f, const Consts& c, uint32_t& even,
+                                          uint32_t& odd) {
     if constexpr (FORMAT == ckpt::kE4M3) {
-        const uint32_t a = __byte_perm(q, 0u, 0x1404), b = __byte_perm(q, 0u, 0x3424);
-        lo = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), f);
-        hi = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), f);
+        even = mul_bf16x2(((q * 16u) & 0x07f007f0u) | ((q * 256u) & 0x80008000u), f);
+        odd = mul_bf16x2(((q >> 4) & 0x07f007f0u) | (q & 0x80008000u), f);
     } else {
-        const uint32_t a = __byte_perm(q, 0u, 0x4140), b = __byte_perm(q, 0u, 0x4342);
-        lo = mul_bf16x2(sub_bf16x2((a & 0x007f007fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u), f);
-        hi = mul_bf16x2(sub_bf16x2((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u), f);
+        const uint32_t o = q >> 8;
+        even = mul_bf16x2(add_bf16x2(and_or(q, 0x007f007fu, c.plus), and_or(q, 0x00800080u, c.minus)), f);
+        odd = mul_bf16x2(add_bf16x2(and_or(o, 0x007f007fu, c.plus), and_or(o, 0x00800080u, c.minus)), f);
     }
 }
 
@@ -424,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int64_t turn_scales = (int64_t)TEAMS * KB * a.c.ld_scales;
         const int64_t turn_data = (int64_t)TEAMS * KB * a.c.ld;
         const int full_blocks = (int)(K / KB);
+        const Consts consts;
         uint32_t turn = 0;        // stages this team has taken: stage = team + TEAMS turn
         uint32_t it = 0;          // stages before this item
         bool ok = true;
@@ -456,10 +479,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     uint32_t f = factor<FORMAT>(codes[j]), f2 = 0u;
                     if constexpr (!one.value) f2 = second_factor<FORMAT>(codes[j], f);
                     uint4 o0, o1;
-                    to_bf16x4<FORMAT>(v.x, f, o0.x, o0.y);
-                    to_bf16x4<FORMAT>(v.y, f, o0.z, o0.w);
-                    to_bf16x4<FORMAT>(v.z, f, o1.x, o1.y);
-                    to_bf16x4<FORMAT>(v.w, f, o1.z, o1.w);
+                    to_bf16x4<FORMAT>(v.x, f, consts, o0.x, o0.y);
+                    to_bf16x4<FORMAT>(v.y, f, consts, o0.z, o0.w);
+                    to_bf16x4<FORMAT>(v.z, f, consts, o1.x, o1.y);
+                    to_bf16x4<FORMAT>(v.w, f, consts, o1.z, o1.w);
                     if constexpr (!one.value) {
                         o0 = make_uint4(mul_bf16x2(o0.x, f2), mul_bf16x2(o0.y, f2),
                                         mul_bf16x2(o0.z, f2), mul_bf16x2(o0.w, f2));
@@ -482,23 +505,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             int left = (int)K - kb * KB - row0;  // rows from this lane's first
             uint4 val[STEPS];       // codes and scale bytes of the team's next stage
             uint32_t codes[STEPS];
+            // (columns past d are read from column 0: whatever they become is not stored)
             auto load = [&]() {
+                if (kb < full_blocks) {
+#pragma unroll
+                    for (int j = 0; j < STEPS; ++j) {
+                        if (j >= STEPS / 2 && !wide) break;
+                        val[j] = __ldg(reinterpret_cast<const uint4*>(dp + j * step_data));
+                        codes[j] = __ldg(sp + j * step_scales);
+                    }
+                    return;
+                }
 #pragma unroll
                 for (int j = 0; j < STEPS; ++j) {
-                    const bool on = in && gap * j < left && (wide || j < STEPS / 2);
+                    const bool on = gap * j < left && (wide || j < STEPS / 2);
                     val[j] = on ? __ldg(reinterpret_cast<const uint4*>(dp + j * step_data)) : make_uint4(0u, 0u, 0u, 0u);
                     codes[j] = on ? __ldg(sp + j * step_scales) : 3u;
                 }
             };
             load();
-            for (; kb < kblocks; kb += TEAMS, ++turn) {
+            for (; kb < kblocks; ++turn) {
                 // the MMAs of the stage STAGES before have read the slot
                 const uint32_t s = team + (turn & 1) * TEAMS;
                 if (!(ok = wait_warp(&sm->used[s], ((turn >> 1) & 1) ^ 1, sm, lim))) break;
                 const uint32_t bt = sbase + OFF_B + s * B_BYTES;
                 uint32_t most = 0;
 #pragma unroll
-                for (int j = 0; j < STEPS; ++j) most = max(most, codes[j]);
+                for (int j = 0; j < STEPS; ++j)
+                    if (wide || j < STEPS / 2) most = max(most, codes[j]);
                 const bool one = kb < full_blocks && !__any_sync(0xffffffffu, most > kOneFactor);
                 if (wide && one)
                     convert(std::true_type{}, std::true_type{}, bt, left, val, codes);
@@ -514,6 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 sp += turn_scales;
                 dp += turn_data;
                 left -= TEAMS * KB;
+                kb += TEAMS;
                 load();
             }
             it += (uint32_t)kblocks;
@@ -549,6 +584,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     const uint32_t box = my_stg + ((ch / BOX) & 1) * STG_BYTES;
                     if (lane == 0) bulk_wait_read1();  // the box before last has been read
                     __syncwarp();
+#pragma unroll
+                    for (int j = 1; j < BOX; j += 4) {  // columns 1 and 2 of every four
+                        const uint32_t x = r[j];
+                        r[j] = r[j + 1];
+                        r[j + 1] = x;
+                    }
                     stage_row(box, lane, r);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
