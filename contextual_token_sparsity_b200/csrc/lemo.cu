@@ -1158,48 +1158,102 @@ lemo::ckpt::View view_of(const lemo_checkpoint* c) {
 const uint4* vecs(const uint16_t* p) { return reinterpret_cast<const uint4*>(p); }
 uint4* vecs(uint16_t* p) { return reinterpret_cast<uint4*>(p); }
 
-// The group shape of a row of dvec 16-byte vectors: the fewest threads times
-// vectors that hold it.
-template <bool BWD, bool POST, int G, int V>
-void launch_norm(const lemo::norm::Args& a, int sms, cudaStream_t st, int* grid_out) {
-    namespace nm = lemo::norm;
-    constexpr int threads = nm::Shape<G, V>::kThreads;
-    int64_t grid = a.rows < 1 ? 1 : a.rows;
-    if (BWD) {
-        if (grid > nm::kMaxParts) grid = nm::kMaxParts;
-        if (grid > 2 * sms) grid = 2 * sms;
-        launch(nm::backward_kernel<G, V, POST>, (unsigned)grid, threads, 0, st, a);
-    } else {
-        if (grid > 4 * sms) grid = 4 * sms;
-        launch(nm::forward_kernel<G, V, POST>, (unsigned)grid, threads, 0, st, a);
+// Sets a kernel's shared-memory limit once per device.
+template <auto Kernel>
+bool allow_smem(int dev, int bytes) {
+    static bool done[kMaxDevices];  // of this kernel
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        done[dev] = true;
     }
-    *grid_out = (int)grid;
+    return true;
 }
 
-template <bool BWD, bool POST>
-lemo_status run_norm(const lemo::norm::Args& a, cudaStream_t st, int* grid) {
+// Adds a stream of rows to the ring of a norm kernel.
+void add_stream(lemo::norm::Args& a, const void* base, int64_t ld_bytes, int64_t bytes, bool by_token) {
+    auto& s = a.in[a.streams++];
+    s.base = static_cast<const uint8_t*>(base);
+    s.ld = ld_bytes;
+    s.bytes = (uint32_t)bytes;
+    s.off = a.slot;
+    s.by_token = by_token ? 1 : 0;
+    a.slot += (uint32_t)bytes;
+}
+
+// The normalised rows of a backward call: bf16 rows, or a checkpoint's codes (a
+// row's copy is rounded up to 16 bytes, which its stride allows).
+void add_source(lemo::norm::Args& a, const uint16_t* rows, int64_t ld, bool by_token,
+                const lemo_checkpoint* c) {
+    if (c)
+        add_stream(a, c->data, c->ld_data, (a.d + 15) / 16 * 16, false);
+    else
+        add_stream(a, rows, 2 * ld, 2 * (int64_t)a.d, by_token);
+}
+
+template <bool BWD, bool POST, bool S2, int G, int V>
+bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* grid_out) {
+    namespace nm = lemo::norm;
+    constexpr int groups = nm::Shape<G>::kGroups;
+    const int64_t stage = (int64_t)a.slot * groups;
+    int64_t stages = (nm::kMaxSmem - nm::kRing) / stage;
+    if (stages > nm::kMaxStages) stages = nm::kMaxStages;
+    a.stages = (int)stages;  // at least two: the largest slot is three rows of kMaxD values
+    int64_t bytes = stages * stage;
+    if (BWD && groups > 1 && bytes < 8 * (int64_t)a.d) bytes = 8 * (int64_t)a.d;  // column sums
+    int64_t grid = a.rows < 1 ? 1 : a.rows;
+    if (grid > sms) grid = sms;
+    if (grid > nm::kMaxParts) grid = nm::kMaxParts;
+    if constexpr (BWD) {
+        if (!allow_smem<nm::backward_kernel<G, V, POST, S2>>(dev, nm::kMaxSmem)) return false;
+        launch(nm::backward_kernel<G, V, POST, S2>, (unsigned)grid, nm::kThreads,
+               nm::kRing + (size_t)bytes, st, a);
+    } else {
+        if (!allow_smem<nm::forward_kernel<G, V, POST>>(dev, nm::kMaxSmem)) return false;
+        launch(nm::forward_kernel<G, V, POST>, (unsigned)grid, nm::kThreads,
+               nm::kRing + (size_t)bytes, st, a);
+    }
+    *grid_out = (int)grid;
+    return true;
+}
+
+// The group of threads that takes a row of dvec 16-byte vectors: the fewest
+// threads that hold it with two or three vectors each (four for the widest rows).
+template <bool BWD, bool POST, bool S2>
+lemo_status run_norm(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     int dev = 0;
     const int sms = device_sms(&dev);
     if (sms <= 0) return LEMO_ERR_CUDA;
-    if (a.dvec <= 32) launch_norm<BWD, POST, 32, 1>(a, sms, st, grid);
-    else if (a.dvec <= 64) launch_norm<BWD, POST, 32, 2>(a, sms, st, grid);
-    else if (a.dvec <= 128) launch_norm<BWD, POST, 64, 2>(a, sms, st, grid);
-    else if (a.dvec <= 256) launch_norm<BWD, POST, 128, 2>(a, sms, st, grid);
-    else if (a.dvec <= 512) launch_norm<BWD, POST, 256, 2>(a, sms, st, grid);
-    else if (a.dvec <= 768) launch_norm<BWD, POST, 256, 3>(a, sms, st, grid);
-    else if (a.dvec <= 1024) launch_norm<BWD, POST, 512, 2>(a, sms, st, grid);
-    else launch_norm<BWD, POST, 512, 4>(a, sms, st, grid);
-    return launch_status();
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        a.spin_limit_ns = (uint64_t)g_spin_ns;
+    }
+    bool ok;
+    if (a.dvec <= 32) ok = launch_norm<BWD, POST, S2, 32, 1>(a, dev, sms, st, grid);
+    else if (a.dvec <= 64) ok = launch_norm<BWD, POST, S2, 32, 2>(a, dev, sms, st, grid);
+    else if (a.dvec <= 128) ok = launch_norm<BWD, POST, S2, 64, 2>(a, dev, sms, st, grid);
+    else if (a.dvec <= 256) ok = launch_norm<BWD, POST, S2, 128, 2>(a, dev, sms, st, grid);
+    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, S2, 256, 2>(a, dev, sms, st, grid);
+    else if (a.dvec <= 768) ok = launch_norm<BWD, POST, S2, 256, 3>(a, dev, sms, st, grid);
+    else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, S2, 512, 2>(a, dev, sms, st, grid);
+    else ok = launch_norm<BWD, POST, S2, 512, 4>(a, dev, sms, st, grid);
+    const lemo_status e = launch_status();
+    return ok ? e : LEMO_ERR_CUDA;
 }
 
 lemo_status run_column_sums(const lemo::norm::Args& n, int parts, const uint16_t* w,
                             const uint16_t* b, const uint16_t* gate, float* dw, float* db,
-                            float* dgate, cudaStream_t st) {
+                            float* dgate, bool second, cudaStream_t st) {
     namespace nm = lemo::norm;
     nm::SumArgs s;
     s.part = n.part;
     s.d = n.d;
     s.max_parts = parts;
+    s.second = second ? 1 : 0;
     s.kept_total = n.kept_total;
     s.rows = n.rows;
     s.w = w;
@@ -1227,6 +1281,7 @@ lemo::norm::Args norm_args(lemo_norm norm, int32_t d, const uint16_t* w, const u
     a.rows = rows;
     a.pad_to = 1;
     a.scale = 1.f;
+    a.src_rows = INT64_MAX;
     a.c.format = lemo::ckpt::kNone;
     return a;
 }
@@ -1303,8 +1358,9 @@ lemo_status lemo_norm_gather(lemo_norm norm, const uint16_t* x, int64_t ld_x, in
     a.stats = reinterpret_cast<float2*>(stats);
     a.pad_to = pad_to;
     a.c = view_of(checkpoint);
+    add_stream(a, x, 2 * ld_x, 2 * (int64_t)d, true);
     int grid = 0;
-    return run_norm<false, false>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
+    return run_norm<false, false, false>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
 }
 
 size_t lemo_norm_workspace_size(int32_t d) {
@@ -1339,16 +1395,19 @@ lemo_status lemo_norm_gather_backward(lemo_norm norm, const uint16_t* dy, int64_
     a.x_rows = dx_rows;
     a.y = vecs(const_cast<uint16_t*>(dy));
     a.ld_y = ld_dy / 8;
-    a.src = vecs(x);
-    a.ld_src = ld_x / 8;
-    a.src_rows = x_rows;
+    if (x) a.src_rows = x_rows;
     a.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
     a.c = view_of(checkpoint);
     a.part = sums ? static_cast<float*>(ws) : nullptr;
+    add_source(a, x, ld_x, true, checkpoint);
+    add_stream(a, dy, 2 * ld_dy, 2 * (int64_t)d, false);
+    add_stream(a, dx, 2 * ld_dx, 2 * (int64_t)d, true);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int grid = 0;
-    if ((e = run_norm<true, false>(a, st, &grid)) != LEMO_OK || !sums) return e;
-    return run_column_sums(a, grid, nullptr, nullptr, nullptr, dweight, dbias, nullptr, st);
+    const bool second = dbias != nullptr;
+    e = second ? run_norm<true, false, true>(a, st, &grid) : run_norm<true, false, false>(a, st, &grid);
+    if (e != LEMO_OK || !sums) return e;
+    return run_column_sums(a, grid, nullptr, nullptr, nullptr, dweight, dbias, nullptr, second, st);
 }
 
 lemo_status lemo_norm_scatter(lemo_norm norm, uint16_t* x, int64_t ld_x, int64_t x_rows, int32_t d,
@@ -1381,8 +1440,11 @@ lemo_status lemo_norm_scatter(lemo_norm norm, uint16_t* x, int64_t ld_x, int64_t
     a.ld_gate = ld_gate / 8;
     a.stats = reinterpret_cast<float2*>(stats);
     a.c = view_of(checkpoint);
+    add_stream(a, y, 2 * ld_y, 2 * (int64_t)d, false);
+    add_stream(a, x, 2 * ld_x, 2 * (int64_t)d, true);
+    if (ld_gate) add_stream(a, gate, 2 * ld_gate, 2 * (int64_t)d, false);
     int grid = 0;
-    return run_norm<false, true>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
+    return run_norm<false, true, false>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
 }
 
 lemo_status lemo_norm_scatter_backward(
@@ -1420,9 +1482,6 @@ lemo_status lemo_norm_scatter_backward(
     a.x_rows = dx_rows;
     a.y = vecs(dy);
     a.ld_y = ld_dy / 8;
-    a.src = vecs(y);
-    a.ld_src = ld_y / 8;
-    a.src_rows = rows;
     a.gate = vecs(gate);
     a.ld_gate = ld_gate / 8;
     a.dgate_rows = vecs(dgate_rows);
@@ -1432,10 +1491,15 @@ lemo_status lemo_norm_scatter_backward(
     a.pad_to = pad_to;
     a.part = sums ? static_cast<float*>(ws) : nullptr;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    add_source(a, y, ld_y, false, checkpoint);
+    add_stream(a, dx, 2 * ld_dx, 2 * (int64_t)d, true);
+    if (ld_gate) add_stream(a, gate, 2 * ld_gate, 2 * (int64_t)d, false);
     int grid = 0;
-    if ((e = run_norm<true, true>(a, st, &grid)) != LEMO_OK || !sums) return e;
+    const bool second = dbias || (dgate && bias);
+    e = second ? run_norm<true, true, true>(a, st, &grid) : run_norm<true, true, false>(a, st, &grid);
+    if (e != LEMO_OK || !sums) return e;
     return run_column_sums(a, grid, weight, bias, ld_gate == 0 ? gate : nullptr, dweight, dbias,
-                           dgate, st);
+                           dgate, second, st);
 }
 
 lemo_status lemo_checkpoint_save(const uint16_t* x, int64_t ld_x, int64_t x_rows,

@@ -18,27 +18,40 @@
 //           a gate of one value per token and channel goes into S1 and S2, and
 //           its gradient rows are dz (vhat w + b).
 //
-// All rows are bf16 and are bound by HBM.  A row belongs to a group of G
-// threads; a thread owns the same V vectors of 8 columns in every row, so
-// weights stay in registers, column sums are per-thread registers, and a row
-// costs one or two reductions over the group.  Rows are dealt to CTAs in a
-// fixed order and the per-CTA column sums are added by a second kernel in CTA
-// order, so every result is deterministic.
+// All rows are bf16; every kernel here is bound by HBM.  One CTA per SM takes
+// rows in a fixed order: a producer warp copies the rows that a stage needs
+// (cp.async.bulk, whole rows) into a ring in shared memory, up to ~200 KB in
+// flight per SM whatever the register use, and NG groups of G threads take one
+// row of each stage.  A thread owns the same V vectors of 8 columns in every
+// row, so weights stay in registers, column sums are per-thread registers, and a
+// row costs one or two reductions over its group.  The CTAs' column sums are
+// added by a second kernel in CTA order, so every result is deterministic.
 #pragma once
 
 #include "ckpt.cuh"
 #include "common.cuh"
+#include "score.cuh"
 
 namespace lemo {
 namespace norm {
 
 using ckpt::pack8;
 using ckpt::unpack8;
+using score::mbar_arrive;
+using score::mbar_arrive_expect_tx;
+using score::mbar_init;
+using score::mbar_try_wait;
+using score::smem_u32;
 
 enum Kind : int { kNoNorm = 0, kRms = 1, kLayer = 2 };
 
-constexpr int kMaxParts = 296;  // CTAs that leave column sums in the workspace
+constexpr int kMaxParts = 296;  // CTAs that leave column sums in the workspace, at most
 constexpr int kMaxD = 16384;
+constexpr int kConsumers = 512; // threads that work on rows; one more warp copies them
+constexpr int kThreads = kConsumers + 32;
+constexpr int kMaxStages = 8;
+constexpr int kMaxGroups = kConsumers / 32;
+constexpr int kMaxSmem = 220 * 1024;
 
 struct Args {
     int kind;
@@ -52,9 +65,7 @@ struct Args {
     // (read by gather, written by scatter)
     uint4* y;
     int64_t ld_y;
-    // backward: the normalised rows, from their bf16 source or from a checkpoint
-    const uint4* src;
-    int64_t ld_src, src_rows;
+    int64_t src_rows;         // backward from bf16 token rows: how many there are
     const uint4* w;           // or nullptr (ones)
     const uint4* b;           // or nullptr (zeros)
     const uint4* gate;        // or nullptr (ones)
@@ -68,20 +79,82 @@ struct Args {
     int pad_to;
     ckpt::View c;             // forward: optional output; backward: source when format >= 0
     float* part;              // [grid][2][d] column sums
+    // the ring
+    int streams, stages;
+    struct {
+        const uint8_t* base;
+        int64_t ld;           // bytes between rows
+        uint32_t bytes, off;  // bytes copied, offset in the row's slot
+        int by_token;         // indexed by token (else by kept row)
+    } in[3];
+    uint32_t slot;            // bytes of one row's slot
+    uint64_t spin_limit_ns;
 };
 
-template <int G, int V>
+struct Smem {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    int64_t token[kMaxStages][kMaxGroups];  // -1: no row, or refused
+    float2 stats[kMaxStages][kMaxGroups];
+    float2 red[2][kConsumers / 32];  // one per consumer warp, two alternating buffers
+    int abort_flag;
+};
+constexpr int kRing = 3072;  // offset of the ring
+static_assert(sizeof(Smem) <= kRing, "the ring starts behind the barriers");
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Smem* sm, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 63) == 0) {
+            if (*reinterpret_cast<volatile int*>(&sm->abort_flag)) return false;
+            if (globaltimer_ns() - t0 > limit_ns) {
+                raise_error(LEMO_ERR_TIMEOUT);
+                *reinterpret_cast<volatile int*>(&sm->abort_flag) = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// Warp-uniform: every lane waits for the phase of the given parity (false: gave up).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Smem* sm, uint64_t limit_ns) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = wait_slow(bar, parity, sm, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+template <int G>
 struct Shape {
-    static constexpr int kThreads = G > 256 ? G : 256;
-    static constexpr int kGroups = kThreads / G;
+    static constexpr int kGroups = kConsumers / G;
     static constexpr int kWarps = G / 32;
 };
 
 // Sums of two values over the G threads of a group, returned to all of them.
 // `red` holds two alternating buffers, so one barrier per call is enough.
-template <int G, int V>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2 (*red)[Shape<G, V>::kWarps],
-                                            int& flip) {
+template <int G>
+__device__ __forceinline__ float2 group_sum(float a, float b, Smem* sm, int& flip) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -90,29 +163,18 @@ __device__ __forceinline__ float2 group_sum(float a, float b, float2 (*red)[Shap
     if constexpr (G == 32) {
         return make_float2(a, b);
     } else {
-        const int warp = (threadIdx.x % G) >> 5;
-        if ((threadIdx.x & 31) == 0) red[flip][warp] = make_float2(a, b);
+        if ((threadIdx.x & 31) == 0) sm->red[flip][threadIdx.x >> 5] = make_float2(a, b);
         asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)(threadIdx.x / G)), "n"(G) : "memory");
         a = b = 0.f;
 #pragma unroll
-        for (int i = 0; i < Shape<G, V>::kWarps; ++i) {
-            a += red[flip][i].x;
-            b += red[flip][i].y;
+        for (int i = 0; i < Shape<G>::kWarps; ++i) {
+            const float2 p = sm->red[flip][threadIdx.x / G * Shape<G>::kWarps + i];
+            a += p.x;
+            b += p.y;
         }
         flip ^= 1;
         return make_float2(a, b);
     }
-}
-
-// Token of kept row r, or -1 (reported) when it is out of range or, for the
-// kernels that update x in place, not above the one before it (two rows of one
-// token would race).
-__device__ __forceinline__ int64_t token_of(const Args& a, int64_t r, bool ascending, bool report) {
-    const int64_t t = a.kept_idx ? a.kept_idx[r] : r;
-    bool ok = t >= 0 && t < a.x_rows;
-    if (ascending && a.kept_idx && r > 0) ok = ok && a.kept_idx[r - 1] < t;
-    if (!ok && report) raise_error(LEMO_ERR_INVALID_ARG);
-    return ok ? t : -1;
 }
 
 __device__ __forceinline__ uint4 ld_or(const uint4* p, int c, bool in, uint32_t other) {
@@ -120,18 +182,115 @@ __device__ __forceinline__ uint4 ld_or(const uint4* p, int c, bool in, uint32_t 
 }
 constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 
+// Row of group g in stage st of this CTA.
+template <int G>
+__device__ __forceinline__ int64_t row_of(int64_t st, int g) {
+    return blockIdx.x + (st * Shape<G>::kGroups + g) * (int64_t)gridDim.x;
+}
+
+// The producer warp: lane g brings the row of group g.
+template <int G>
+__device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, int64_t K,
+                                        bool ascending, bool want_stats) {
+    constexpr int NG = Shape<G>::kGroups;
+    const int lane = threadIdx.x & 31;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    int64_t st = 0;
+    for (; row_of<G>(st, 0) < K; ++st) {
+        // this stage's token and statistics, read while the slot may still be in use
+        const int64_t r = row_of<G>(st, lane);
+        int64_t t = -1;
+        float2 stat = make_float2(0.f, 1.f);
+        if (lane < NG && r < K) {
+            t = a.kept_idx ? a.kept_idx[r] : r;
+            bool good = t >= 0 && t < a.x_rows && t < a.src_rows;
+            // two rows of one token would race in the kernels that update token rows
+            if (ascending && a.kept_idx && r > 0) good = good && a.kept_idx[r - 1] < t;
+            if (!good) {
+                raise_error(LEMO_ERR_INVALID_ARG);
+                t = -1;
+            }
+            if (want_stats) stat = a.stats[r];
+        }
+        if (!(ok = wait_warp(&sm->empty[s], ph ^ 1, sm, a.spin_limit_ns))) break;
+        const uint32_t rows = __ballot_sync(0xffffffffu, t >= 0);
+        if (lane < NG) {
+            sm->token[s][lane] = t;
+            sm->stats[s][lane] = stat;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            uint32_t bytes = 0;
+            for (int i = 0; i < a.streams; ++i) bytes += a.in[i].bytes;
+            mbar_arrive_expect_tx(&sm->full[s], bytes * (uint32_t)__popc(rows));
+        }
+        __syncwarp();
+        if (t >= 0) {
+            const uint32_t dst = ring + (uint32_t)(s * NG + lane) * a.slot;
+            for (int i = 0; i < a.streams; ++i)
+                bulk_load(dst + a.in[i].off, a.in[i].base + (a.in[i].by_token ? t : r) * a.in[i].ld,
+                          a.in[i].bytes, &sm->full[s]);
+        }
+        if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+    if (!ok) {  // every copy in flight lands before the CTA leaves
+        for (int64_t j = st > a.stages ? st - a.stages : 0; j < st; ++j) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&sm->full[j % a.stages], (uint32_t)(j / a.stages) & 1) &&
+                   globaltimer_ns() - t0 < a.spin_limit_ns) {
+            }
+        }
+    }
+}
+
+template <int G>
+__device__ __forceinline__ void init_ring(const Args& a, Smem* sm) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], kConsumers / 32);
+        }
+        sm->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+}
+
+// Zero rows [K, K_pad) of the kept-row output.
+__device__ __forceinline__ void zero_tail(const Args& a, int64_t K, int64_t K_pad) {
+    const int64_t n = (K_pad - K) * a.dvec;
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * kThreads)
+        a.y[(K + i / a.dvec) * a.ld_y + i % a.dvec] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // ---------------------------------------------------------------------------
-// Forward
+// Forward.  Streams: gather x; scatter y, x, (gate rows).
 // ---------------------------------------------------------------------------
 template <int G, int V, bool POST>
-__global__ void __launch_bounds__(Shape<G, V>::kThreads) forward_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Smem* sm = reinterpret_cast<Smem*>(smem_raw);
+    init_ring<G>(a, sm);
     pdl_entry();
-    using S = Shape<G, V>;
-    __shared__ float2 red_s[S::kGroups][2][S::kWarps];
+    constexpr int NG = Shape<G>::kGroups;
+    const uint32_t ring = smem_u32(smem_raw) + kRing;
+    const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
+    if (!POST) {
+        const int64_t K_pad = ckpt::clamp_pad(K, a.pad_to, a.rows);
+        if (K_pad > K) zero_tail(a, K, K_pad);
+    }
+    if (threadIdx.x >= kConsumers) {
+        produce<G>(a, sm, ring, K, POST, false);
+        return;
+    }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
     int flip = 0;
-    const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
-    const int64_t K_pad = POST ? K : ckpt::clamp_pad(K, a.pad_to, a.rows);
     uint4 w[V], b[V], gate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -140,213 +299,284 @@ __global__ void __launch_bounds__(Shape<G, V>::kThreads) forward_kernel(const Ar
         b[v] = ld_or(a.b, c, c < a.dvec, 0u);
         if (POST) gate[v] = ld_or(a.ld_gate == 0 ? a.gate : nullptr, c, c < a.dvec, kOnes);
     }
-    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * group; r < K_pad;
-         r += (int64_t)gridDim.x * S::kGroups) {
-        if (r >= K) {
+    int s = 0;
+    uint32_t ph = 0;
+    for (int64_t st = 0; row_of<G>(st, 0) < K; ++st) {
+        if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
+        const int64_t t = sm->token[s][group];
+        if (t >= 0) {
+            const int64_t r = row_of<G>(st, group);
+            const uint32_t row = ring + (uint32_t)(s * NG + group) * a.slot;
+            uint4 in[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
-                if (c < a.dvec) a.y[r * a.ld_y + c] = make_uint4(0u, 0u, 0u, 0u);
+                in[v] = c < a.dvec ? ld_shared(row + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
             }
-            continue;
-        }
-        const int64_t t = token_of(a, r, POST, i == 0);
-        if (t < 0) continue;
-        const uint4* row = POST ? a.y + r * a.ld_y : a.x + t * a.ld_x;
-        uint4 in[V];
+            float mean = 0.f, rstd = 1.f;
+            if (a.kind != kNoNorm) {
+                if (a.kind == kLayer) {
+                    float sum = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * G + i;
-            in[v] = c < a.dvec ? row[c] : make_uint4(0u, 0u, 0u, 0u);
-        }
-        float mean = 0.f, rstd = 1.f;
-        if (a.kind != kNoNorm) {
-            if (a.kind == kLayer) {
-                float s = 0.f;
+                    for (int v = 0; v < V; ++v) {
+                        float f[8];
+                        unpack8(in[v], f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum += f[j];
+                    }
+                    mean = group_sum<G>(sum, 0.f, sm, flip).x * a.inv_d;
+                }
+                float sum = 0.f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float f[8];
                     unpack8(in[v], f);
+                    if (v * G + i < a.dvec) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s += f[j];
+                        for (int j = 0; j < 8; ++j) sum += (f[j] - mean) * (f[j] - mean);
+                    }
                 }
-                mean = group_sum<G, V>(s, 0.f, red_s[group], flip).x * a.inv_d;
+                rstd = 1.f / sqrtf(group_sum<G>(sum, 0.f, sm, flip).x * a.inv_d + a.eps);
             }
-            float s = 0.f;
+            if (a.stats && i == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float f[8];
+                const int c = v * G + i;
+                if (a.c.format >= 0) {
+                    const uint32_t code = ckpt::scale_code(in[v], a.c.format);
+                    if (c < a.dvec) ckpt::store8(a.c, r, c, in[v], code);
+                }
+                if (c >= a.dvec) continue;
+                float f[8], wf[8], bf[8];
                 unpack8(in[v], f);
-                if (v * G + i < a.dvec) {
+                unpack8(w[v], wf);
+                unpack8(b[v], bf);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s += (f[j] - mean) * (f[j] - mean);
+                for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd * wf[j] + bf[j];
+                if (POST) {
+                    float gf[8], xf[8];
+                    unpack8(a.streams == 3 ? ld_shared(row + a.in[2].off + 16 * c) : gate[v], gf);
+                    unpack8(ld_shared(row + a.in[1].off + 16 * c), xf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) xf[j] += a.scale * (gf[j] * f[j]);
+                    a.x[t * a.ld_x + c] = pack8(xf);
+                } else {
+                    a.y[r * a.ld_y + c] = pack8(f);
                 }
             }
-            rstd = 1.f / sqrtf(group_sum<G, V>(s, 0.f, red_s[group], flip).x * a.inv_d + a.eps);
         }
-        if (a.stats && i == 0) a.stats[r] = make_float2(mean, rstd);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * G + i;
-            if (a.c.format >= 0) {
-                const uint32_t code = ckpt::scale_code(in[v], a.c.format);
-                if (c < a.dvec) ckpt::store8(a.c, r, c, in[v], code);
-            }
-            if (c >= a.dvec) continue;
-            float f[8], wf[8], bf[8];
-            unpack8(in[v], f);
-            unpack8(w[v], wf);
-            unpack8(b[v], bf);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd * wf[j] + bf[j];
-            if (POST) {
-                float gf[8], xf[8];
-                unpack8(a.gate && a.ld_gate ? __ldg(a.gate + r * a.ld_gate + c) : gate[v], gf);
-                uint4* xp = a.x + t * a.ld_x + c;
-                unpack8(*xp, xf);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) xf[j] += a.scale * (gf[j] * f[j]);
-                *xp = pack8(xf);
-            } else {
-                a.y[r * a.ld_y + c] = pack8(f);
-            }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->empty[s]);
+        if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Backward
+// Backward.  Streams: the normalised row (bf16 or codes); gather dy, dx;
+// scatter dx, (gate rows).  S2: the sums of dy (dn) are wanted too.
 // ---------------------------------------------------------------------------
-template <int G, int V, bool POST>
-__global__ void __launch_bounds__(Shape<G, V>::kThreads) backward_kernel(const Args a) {
+template <int G, int V, bool POST, bool S2>
+__global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Smem* sm = reinterpret_cast<Smem*>(smem_raw);
+    init_ring<G>(a, sm);
     pdl_entry();
-    using S = Shape<G, V>;
-    __shared__ float2 red_s[S::kGroups][2][S::kWarps];
-    __shared__ float acc_s[S::kGroups > 1 ? 2 * 8 * G * V : 1];
+    constexpr int NG = Shape<G>::kGroups;
+    const uint32_t ring = smem_u32(smem_raw) + kRing;
+    const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
+    if (POST) {
+        const int64_t K_pad = ckpt::clamp_pad(K, a.pad_to, a.rows);
+        if (K_pad > K) zero_tail(a, K, K_pad);
+    }
+    if (threadIdx.x >= kConsumers) {
+        produce<G>(a, sm, ring, K, !POST, a.kind != kNoNorm);
+        return;
+    }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
     int flip = 0;
-    const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
-    const int64_t K_pad = POST ? ckpt::clamp_pad(K, a.pad_to, a.rows) : K;
-    float s1[8 * V], s2[8 * V];
+    const bool coded = a.c.format >= 0;
+    uint4 w[V];
+    float s1[8 * V], s2[S2 ? 8 * V : 1];
 #pragma unroll
-    for (int j = 0; j < 8 * V; ++j) s1[j] = s2[j] = 0.f;
-    for (int64_t r = blockIdx.x + (int64_t)gridDim.x * group; r < K_pad;
-         r += (int64_t)gridDim.x * S::kGroups) {
-        if (r >= K) {
+    for (int v = 0; v < V; ++v) w[v] = ld_or(a.w, v * G + i, v * G + i < a.dvec, kOnes);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * G + i;
-                if (c < a.dvec) a.y[r * a.ld_y + c] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            continue;
-        }
-        int64_t t = token_of(a, r, !POST, i == 0);
-        if (!POST && a.c.format < 0 && t >= a.src_rows) {
-            if (i == 0) raise_error(LEMO_ERR_INVALID_ARG);
-            t = -1;
-        }
-        if (t < 0) continue;
-        float mean = 0.f, rstd = 1.f;
-        if (a.kind != kNoNorm) {
-            const float2 st = a.stats[r];
-            mean = st.x;
-            rstd = st.y;
-        }
-        // vhat and g of this row
-        float vh[8 * V], g[8 * V];
-        float p1 = 0.f, p2 = 0.f;
+    for (int j = 0; j < 8 * V; ++j) {
+        s1[j] = 0.f;
+        if (S2) s2[j] = 0.f;
+    }
+    // scale bytes of this group's next row
+    uint32_t code[V];
+    auto load_codes = [&](int64_t r) {
+        if (!coded || r >= K) return;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * G + i;
-            float* vv = vh + 8 * v;
-            float* gg = g + 8 * v;
-            if (c >= a.dvec) {
+            code[v] = c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
+        }
+    };
+    load_codes(row_of<G>(0, group));
+    int s = 0;
+    uint32_t ph = 0;
+    for (int64_t st = 0; row_of<G>(st, 0) < K; ++st) {
+        if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
+        const int64_t t = sm->token[s][group];
+        const int64_t r = row_of<G>(st, group);
+        if (t >= 0) {
+            const uint32_t row = ring + (uint32_t)(s * NG + group) * a.slot;
+            const float2 stat = sm->stats[s][group];
+            const float mean = stat.x, rstd = stat.y;
+            // The row's raw vectors stay in registers over the reduction, not what they unpack
+            // to (a third of the registers); both passes unpack them.
+            uint4 raw_v[V], raw_g[V];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) vv[j] = gg[j] = 0.f;
-                continue;
-            }
-            if (a.c.format >= 0)
-                ckpt::load8(a.c, r, c, vv);
-            else
-                unpack8(__ldg(a.src + (POST ? r : t) * a.ld_src + c), vv);
-            float wf[8];
-            unpack8(ld_or(a.w, c, true, kOnes), wf);
-            unpack8(POST ? a.x[t * a.ld_x + c] : a.y[r * a.ld_y + c], gg);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) vv[j] = (vv[j] - mean) * rstd;
-            if (POST) {
-                float gf[8];
-                unpack8(ld_or(a.gate ? a.gate + r * a.ld_gate : nullptr, c, true, kOnes), gf);
-                float bf[8], dgf[8];
-                if (a.dgate_rows) unpack8(ld_or(a.b, c, true, 0u), bf);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float dz = a.scale * gg[j], dn = dz * gf[j];
-                    const float sum = a.ld_gate ? dn : dz;
-                    s1[8 * v + j] += sum * vv[j];
-                    s2[8 * v + j] += sum;
-                    if (a.dgate_rows) dgf[j] = dz * (vv[j] * wf[j] + bf[j]);
-                    gg[j] = dn * wf[j];
+            for (int v = 0; v < V; ++v) {
+                const int c = v * G + i;
+                raw_v[v] = raw_g[v] = make_uint4(0u, 0u, 0u, 0u);
+                if (c >= a.dvec) continue;
+                if (coded) {
+                    const uint2 q = ld_shared8(row + 8 * c);
+                    raw_v[v].x = q.x;
+                    raw_v[v].y = q.y;
+                } else {
+                    raw_v[v] = ld_shared(row + 16 * c);
                 }
-                if (a.dgate_rows) a.dgate_rows[r * a.ld_dgate + c] = pack8(dgf);
-            } else {
+                raw_g[v] = ld_shared(row + a.in[1].off + 16 * c);
+            }
+            auto vhat = [&](int v, float* f) {
+                if (coded)
+                    ckpt::decode8(make_uint2(raw_v[v].x, raw_v[v].y), code[v], a.c.format, f);
+                else
+                    unpack8(raw_v[v], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd;
+            };
+            // gate of vector v (POST)
+            auto gated = [&](int v, float* gf) {
+                const int c = v * G + i;
+                unpack8(a.ld_gate ? ld_shared(row + a.in[2].off + 16 * c) : ld_or(a.gate, c, true, kOnes),
+                        gf);
+            };
+            float p1 = 0.f, p2 = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = v * G + i;
+                if (c >= a.dvec) continue;
+                float vv[8], gg[8], wf[8];
+                vhat(v, vv);
+                unpack8(raw_g[v], gg);
+                unpack8(w[v], wf);
+                if (POST) {
+                    float gf[8];
+                    gated(v, gf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) gg[j] *= a.scale;
+                    if (a.dgate_rows) {
+                        float bf[8];
+                        unpack8(ld_or(a.b, c, true, 0u), bf);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) bf[j] = gg[j] * (vv[j] * wf[j] + bf[j]);
+                        a.dgate_rows[r * a.ld_dgate + c] = pack8(bf);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float dn = gg[j] * gf[j];
+                        const float sum = a.ld_gate ? dn : gg[j];
+                        s1[8 * v + j] += sum * vv[j];
+                        if (S2) s2[8 * v + j] += sum;
+                        gg[j] = dn;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        s1[8 * v + j] += gg[j] * vv[j];
+                        if (S2) s2[8 * v + j] += gg[j];
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    s1[8 * v + j] += gg[j] * vv[j];
-                    s2[8 * v + j] += gg[j];
                     gg[j] *= wf[j];
+                    p1 += gg[j] * vv[j];
+                    p2 += gg[j];
                 }
             }
+            float c1 = 0.f, c2 = 0.f;
+            if (a.kind != kNoNorm) {
+                const float2 p = group_sum<G>(p1, p2, sm, flip);
+                c1 = p.x * a.inv_d;
+                c2 = a.kind == kLayer ? p.y * a.inv_d : 0.f;
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                p1 += gg[j] * vv[j];
-                p2 += gg[j];
+            for (int v = 0; v < V; ++v) {
+                const int c = v * G + i;
+                if (c >= a.dvec) continue;
+                // opaque: or the compiler keeps the unpacked values of the first pass instead
+                asm volatile("" : "+r"(raw_v[v].x), "+r"(raw_v[v].y), "+r"(raw_v[v].z), "+r"(raw_v[v].w),
+                             "+r"(raw_g[v].x), "+r"(raw_g[v].y), "+r"(raw_g[v].z), "+r"(raw_g[v].w));
+                float vv[8], gg[8], wf[8];
+                vhat(v, vv);
+                unpack8(raw_g[v], gg);
+                unpack8(w[v], wf);
+                if (POST) {
+                    float gf[8];
+                    gated(v, gf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) gg[j] = gg[j] * a.scale * gf[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) gg[j] = rstd * (gg[j] * wf[j] - vv[j] * c1 - c2);
+                if (POST) {
+                    a.y[r * a.ld_y + c] = pack8(gg);
+                } else {
+                    float xf[8];
+                    unpack8(ld_shared(row + a.in[2].off + 16 * c), xf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) gg[j] += xf[j];
+                    a.x[t * a.ld_x + c] = pack8(gg);
+                }
             }
         }
-        float c1 = 0.f, c2 = 0.f;
-        if (a.kind != kNoNorm) {
-            const float2 p = group_sum<G, V>(p1, p2, red_s[group], flip);
-            c1 = p.x * a.inv_d;
-            c2 = a.kind == kLayer ? p.y * a.inv_d : 0.f;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->empty[s]);
+        load_codes(row_of<G>(st + 1, group));
+        if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
         }
+    }
+    if (!a.part || blockIdx.x >= K) return;
+    // column sums of this CTA: its groups in order, through the ring (every copy was consumed)
+    if constexpr (NG > 1) {
+        float* acc = reinterpret_cast<float*>(smem_raw + kRing);
+        for (int gi = 0; gi < NG; ++gi) {
+            asm volatile("bar.sync 15, %0;" ::"n"(kConsumers) : "memory");
+            if (gi == group) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int c = v * G + i;
+                    if (c >= a.dvec) continue;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        // column 8 c + j at [j][c]: neighbouring threads in neighbouring words
+                        const int at = j * a.dvec + c;
+                        acc[at] = gi ? acc[at] + s1[8 * v + j] : s1[8 * v + j];
+                        if (S2) acc[a.d + at] = gi ? acc[a.d + at] + s2[8 * v + j] : s2[8 * v + j];
+                    }
+                }
+            }
+        }
+        if (group != NG - 1) return;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * G + i;
             if (c >= a.dvec) continue;
-            float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = rstd * (g[8 * v + j] - vh[8 * v + j] * c1 - c2);
-            if (POST) {
-                a.y[r * a.ld_y + c] = pack8(f);
-            } else {
-                uint4* xp = a.x + t * a.ld_x + c;
-                float xf[8];
-                unpack8(*xp, xf);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += xf[j];
-                *xp = pack8(f);
+            for (int j = 0; j < 8; ++j) {
+                s1[8 * v + j] = acc[j * a.dvec + c];
+                if (S2) s2[8 * v + j] = acc[a.d + j * a.dvec + c];
             }
-        }
-    }
-    if (!a.part || blockIdx.x >= K) return;
-    // column sums of this CTA: its groups in order
-    if constexpr (S::kGroups > 1) {
-        for (int gi = 0; gi < S::kGroups; ++gi) {
-            __syncthreads();
-            if (gi == group) {
-#pragma unroll
-                for (int j = 0; j < 8 * V; ++j) {
-                    const int at = j * G + i;
-                    acc_s[at] = gi ? acc_s[at] + s1[j] : s1[j];
-                    acc_s[8 * G * V + at] = gi ? acc_s[8 * G * V + at] + s2[j] : s2[j];
-                }
-            }
-        }
-        if (group != S::kGroups - 1) return;
-#pragma unroll
-        for (int j = 0; j < 8 * V; ++j) {
-            s1[j] = acc_s[j * G + i];
-            s2[j] = acc_s[8 * G * V + j * G + i];
         }
     }
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
@@ -358,15 +588,16 @@ __global__ void __launch_bounds__(Shape<G, V>::kThreads) backward_kernel(const A
         for (int j = 0; j < 8; j += 4) {
             *reinterpret_cast<float4*>(part + 8 * c + j) =
                 make_float4(s1[8 * v + j], s1[8 * v + j + 1], s1[8 * v + j + 2], s1[8 * v + j + 3]);
-            *reinterpret_cast<float4*>(part + a.d + 8 * c + j) =
-                make_float4(s2[8 * v + j], s2[8 * v + j + 1], s2[8 * v + j + 2], s2[8 * v + j + 3]);
+            if (S2)
+                *reinterpret_cast<float4*>(part + a.d + 8 * c + j) =
+                    make_float4(s2[8 * v + j], s2[8 * v + j + 1], s2[8 * v + j + 2], s2[8 * v + j + 3]);
         }
     }
 }
 
 struct SumArgs {
     const float* part;  // [parts][2][d]
-    int d, max_parts;
+    int d, max_parts, second;  // second: the sums of dy (dn) are there too
     const int32_t* kept_total;
     int64_t rows;
     const uint16_t* w;     // of dgate
@@ -398,7 +629,7 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sums_kernel(cons
         for (int p = slice; p < parts; p += kSumSlices) {
             const float* row = a.part + (int64_t)p * 2 * a.d;
             s.x += row[c];
-            s.y += row[a.d + c];
+            if (a.second) s.y += row[a.d + c];
         }
     }
     acc[slice][col] = s;
