@@ -145,6 +145,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object per call
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -297,65 +300,77 @@ def lemo_segment_loss(h, w, targets, seg_rows, loss, ws, token_loss=None, dh=Non
 # the current CUDA device and has the type, row layout and sizes the call
 # needs; a tensor that does not fit raises LemoError(LEMO_ERR_INVALID_ARG).
 # ---------------------------------------------------------------------------
+_BF16 = _FP32 = _INT32 = _UINT8 = None  # torch dtypes, set with the first _Fit
+
+
 class _Fit:
-    """Tensor checks of one call: ``fit(...)`` returns the data pointer."""
+    """Tensor checks of one call: its methods return the data pointer."""
 
     __slots__ = ("where", "dev")
 
     def __init__(self, where: str):
-        import torch
+        if _BF16 is None:
+            _bind_torch()
         self.where = where
-        self.dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+        self.dev = _device()
 
-    def _bad(self, name, why):
+    def bad(self, name, why):
         err = LemoError(LEMO_ERR_INVALID_ARG, self.where)
         err.args = (f"{self.where}: {name} {why}",)
         raise err
 
     def mat(self, t, name, dtype, cols, rows=0):
         if t is None:
-            self._bad(name, "is missing")
-        if str(t.dtype) != dtype or t.dim() != 2:
-            self._bad(name, f"is not a 2-D {dtype} tensor")
+            self.bad(name, "is missing")
+        if t.dtype is not dtype or t.dim() != 2:
+            self.bad(name, f"is not a 2-D {dtype} tensor")
         if t.get_device() != self.dev:
-            self._bad(name, "is not on the current CUDA device")
+            self.bad(name, "is not on the current CUDA device")
         n, width = t.shape
         if n < rows or width < cols:
-            self._bad(name, f"has shape {(n, width)}, at least {(rows, cols)} is needed")
+            self.bad(name, f"has shape {(n, width)}, at least {(rows, cols)} is needed")
         if width > 1 and t.stride(1) != 1:
-            self._bad(name, "does not have contiguous rows")
+            self.bad(name, "does not have contiguous rows")
         return t.data_ptr()
 
     def vec(self, t, name, dtype, n):
         if t is None:
             return None
-        if str(t.dtype) != dtype or t.dim() != 1 or t.shape[0] < n:
-            self._bad(name, f"is not a 1-D {dtype} tensor of at least {n} values")
+        if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n:
+            self.bad(name, f"is not a 1-D {dtype} tensor of at least {n} values")
         if t.get_device() != self.dev:
-            self._bad(name, "is not on the current CUDA device")
-        if n > 1 and t.stride(0) != 1:
-            self._bad(name, "is not contiguous")
+            self.bad(name, "is not on the current CUDA device")
+        if n != 1 and t.stride(0) != 1 and t.shape[0] > 1:
+            self.bad(name, "is not contiguous")
         return t.data_ptr()
 
-    def idx(self, kept_idx, kept_total):
+    def total(self, kept_total):
         if kept_total is None:
-            self._bad("kept_total", "is missing")
-        return (self.vec(kept_idx, "kept_idx", _INT32, 0),
-                self.vec(kept_total, "kept_total", _INT32, 1))
+            self.bad("kept_total", "is missing")
+        return self.vec(kept_total, "kept_total", _INT32, 1)
 
     def ckpt(self, c, name, d, rows):
         if c is None:
             return None
         if not isinstance(c, Checkpoint):
-            self._bad(name, "is not a Checkpoint")
+            self.bad(name, "is not a Checkpoint")
         if c.device != self.dev:
-            self._bad(name, "is not on the current CUDA device")
+            self.bad(name, "is not on the current CUDA device")
         if c.d != d or c.rows < rows:
-            self._bad(name, f"holds {(c.rows, c.d)}, at least {(rows, d)} is needed")
+            self.bad(name, f"holds {(c.rows, c.d)}, at least {(rows, d)} is needed")
         return c.ref
 
 
-_BF16, _FP32, _INT32, _UINT8 = "torch.bfloat16", "torch.float32", "torch.int32", "torch.uint8"
+def _bind_torch():
+    global _BF16, _FP32, _INT32, _UINT8
+    import torch
+    _BF16, _FP32, _INT32, _UINT8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _device() -> int:
+    """Current CUDA device, or -2 where CUDA is not in use (no tensor is on it)."""
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
 def _ld(t, unit=8):
@@ -392,7 +407,7 @@ def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y
     fit = _Fit("lemo_norm_gather")
     d = x.shape[1] if d is None else d
     xp, yp, rows = fit.mat(x, "x", _BF16, d), fit.mat(y, "y", _BF16, d), y.shape[0]
-    ip, kp = fit.idx(kept_idx, kept_total)
+    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
     _check(load().lemo_norm_gather(
         int(norm), xp, _ld(x), x.shape[0], int(d), fit.vec(weight, "weight", _BF16, d),
         fit.vec(bias, "bias", _BF16, d), float(eps), ip, kp, int(pad_to), yp, _ld(y), rows,
@@ -405,17 +420,17 @@ def _stats(fit, stats, rows):
         return None
     p = fit.mat(stats, "stats", _FP32, 2, rows)
     if stats.shape[1] != 2 or (rows > 1 and stats.stride(0) != 2):
-        fit._bad("stats", "is not a contiguous [rows, 2] tensor")
+        fit.bad("stats", "is not a contiguous [rows, 2] tensor")
     return p
 
 
 def _workspace(fit, ws, needed):
     if ws is None:
         if needed:
-            fit._bad("ws", "is missing")
+            fit.bad("ws", "is missing")
         return None, 0
     if ws.get_device() != fit.dev or not ws.is_contiguous():
-        fit._bad("ws", "is not a contiguous tensor on the current CUDA device")
+        fit.bad("ws", "is not a contiguous tensor on the current CUDA device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -432,7 +447,7 @@ def lemo_norm_gather_backward(norm, dy, weight, stats, kept_idx, kept_total, dx,
     d = dy.shape[1] if d is None else d
     rows = dy.shape[0]
     dyp, dxp = fit.mat(dy, "dy", _BF16, d), fit.mat(dx, "dx", _BF16, d)
-    ip, kp = fit.idx(kept_idx, kept_total)
+    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
     wsp, ws_bytes = _workspace(fit, ws, dweight is not None or dbias is not None)
     _check(load().lemo_norm_gather_backward(
         int(norm), dyp, _ld(dy), rows, int(d), fit.vec(weight, "weight", _BF16, d),
@@ -459,7 +474,7 @@ def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept
     d = x.shape[1] if d is None else d
     rows = y.shape[0]
     xp, yp = fit.mat(x, "x", _BF16, d), fit.mat(y, "y", _BF16, d)
-    ip, kp = fit.idx(kept_idx, kept_total)
+    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
     gp, ld_gate = _gate(fit, gate, d, rows)
     _check(load().lemo_norm_scatter(
         int(norm), xp, _ld(x), x.shape[0], int(d), yp, _ld(y), rows,
@@ -479,7 +494,7 @@ def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_
     d = dx.shape[1] if d is None else d
     rows = dy.shape[0]
     dxp, dyp = fit.mat(dx, "dx", _BF16, d), fit.mat(dy, "dy", _BF16, d)
-    ip, kp = fit.idx(kept_idx, kept_total)
+    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
     gp, ld_gate = _gate(fit, gate, d, rows)
     per_row = dgate is not None and dgate.dim() == 2
     dg = None if per_row else fit.vec(dgate, "dgate", _FP32, d)
@@ -499,7 +514,7 @@ def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
     """x bf16 [tokens, >= checkpoint.d]; kept_idx int32 or None (row r is token r)."""
     fit = _Fit("lemo_checkpoint_save")
     d = checkpoint.d
-    ip, kp = fit.idx(kept_idx, kept_total)
+    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
     _check(load().lemo_checkpoint_save(fit.mat(x, "x", _BF16, d), _ld(x), x.shape[0], ip, kp,
                                        fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream)),
            "lemo_checkpoint_save")
@@ -509,7 +524,7 @@ def lemo_checkpoint_restore(checkpoint, kept_total, pad_to, y, stream=None):
     """y bf16 [rows, >= checkpoint.d], rows <= checkpoint.rows."""
     fit = _Fit("lemo_checkpoint_restore")
     d = checkpoint.d
-    _, kp = fit.idx(None, kept_total)
+    kp = fit.total(kept_total)
     yp = fit.mat(y, "y", _BF16, d)
     _check(load().lemo_checkpoint_restore(fit.ckpt(checkpoint, "checkpoint", d, y.shape[0]), kp,
                                           int(pad_to), yp, _ld(y), y.shape[0], _stream(stream)),
@@ -522,7 +537,7 @@ def lemo_gated_mlp(gate, up, kept_total, pad_to, a, gate_checkpoint=None, up_che
     fit = _Fit("lemo_gated_mlp")
     d = a.shape[1] if d is None else d
     rows = a.shape[0]
-    _, kp = fit.idx(None, kept_total)
+    kp = fit.total(kept_total)
     _check(load().lemo_gated_mlp(
         fit.mat(gate, "gate", _BF16, d, rows), _ld(gate), fit.mat(up, "up", _BF16, d, rows),
         _ld(up), int(d), kp, int(pad_to), fit.mat(a, "a", _BF16, d), _ld(a), rows,
@@ -536,7 +551,7 @@ def lemo_gated_mlp_backward(gate_checkpoint, up_checkpoint, da, kept_total, pad_
     """da, dgate, dup and the optional recomputed activation a: bf16 [rows, >= d]."""
     fit = _Fit("lemo_gated_mlp_backward")
     d, rows = gate_checkpoint.d, dgate.shape[0]
-    _, kp = fit.idx(None, kept_total)
+    kp = fit.total(kept_total)
     _check(load().lemo_gated_mlp_backward(
         fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
         fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), fit.mat(da, "da", _BF16, d, rows),
@@ -551,7 +566,7 @@ def lemo_checkpoint_weight_grad(checkpoint, dy, kept_total, dw, stream=None, n=N
     fit = _Fit("lemo_checkpoint_weight_grad")
     d, rows = checkpoint.d, dy.shape[0]
     n = dy.shape[1] if n is None else n
-    _, kp = fit.idx(None, kept_total)
+    kp = fit.total(kept_total)
     _check(load().lemo_checkpoint_weight_grad(
         fit.ckpt(checkpoint, "checkpoint", d, rows), fit.mat(dy, "dy", _BF16, n), _ld(dy), rows,
         int(n), kp, fit.mat(dw, "dw", _FP32, d, n), _ld(dw, 4), _stream(stream)),
