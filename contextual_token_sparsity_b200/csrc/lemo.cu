@@ -1195,36 +1195,39 @@ void add_source(lemo::norm::Args& a, const uint16_t* rows, int64_t ld, bool by_t
         add_stream(a, rows, 2 * ld, 2 * (int64_t)a.d, by_token);
 }
 
-template <bool BWD, bool POST, bool S2, int G, int V>
+template <bool BWD, bool POST, bool S2, typename S>
 bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* grid_out) {
     namespace nm = lemo::norm;
-    constexpr int groups = nm::Shape<G>::kGroups;
-    const int64_t stage = (int64_t)a.slot * groups;
+    const int64_t stage = (int64_t)a.slot * S::kRows;
     int64_t stages = (nm::kMaxSmem - nm::kRing) / stage;
     if (stages > nm::kMaxStages) stages = nm::kMaxStages;
-    a.stages = (int)stages;  // at least two: the largest slot is three rows of kMaxD values
+    if (stages < 1) return false;  // not reached: see the shapes in run_norm
+    a.stages = (int)stages;
     int64_t bytes = stages * stage;
-    if (BWD && groups > 1 && bytes < 8 * (int64_t)a.d) bytes = 8 * (int64_t)a.d;  // column sums
+    if (BWD && S::kGroups > 1 && bytes < 8 * (int64_t)a.d) bytes = 8 * (int64_t)a.d;  // column sums
     int64_t grid = a.rows < 1 ? 1 : a.rows;
     if (grid > sms) grid = sms;
     if (grid > nm::kMaxParts) grid = nm::kMaxParts;
     if constexpr (BWD) {
-        if (!allow_smem<nm::backward_kernel<G, V, POST, S2>>(dev, nm::kMaxSmem)) return false;
-        launch(nm::backward_kernel<G, V, POST, S2>, (unsigned)grid, nm::kThreads,
-               nm::kRing + (size_t)bytes, st, a);
+        if (!allow_smem<nm::backward_kernel<S, POST, S2>>(dev, nm::kMaxSmem)) return false;
+        launch(nm::backward_kernel<S, POST, S2>, (unsigned)grid, S::kThreads, nm::kRing + (size_t)bytes,
+               st, a);
     } else {
-        if (!allow_smem<nm::forward_kernel<G, V, POST>>(dev, nm::kMaxSmem)) return false;
-        launch(nm::forward_kernel<G, V, POST>, (unsigned)grid, nm::kThreads,
-               nm::kRing + (size_t)bytes, st, a);
+        if (!allow_smem<nm::forward_kernel<S, POST>>(dev, nm::kMaxSmem)) return false;
+        launch(nm::forward_kernel<S, POST>, (unsigned)grid, S::kThreads, nm::kRing + (size_t)bytes, st,
+               a);
     }
     *grid_out = (int)grid;
     return true;
 }
 
-// The group of threads that takes a row of dvec 16-byte vectors: the fewest
-// threads that hold it with two or three vectors each (four for the widest rows).
+// The group of threads that takes a row of dvec 16-byte vectors: one vector per
+// thread up to 640 threads, then 512 threads with two or four.  Rows per group and
+// stage: as many as keep at least two stages in the ring (a row is up to three
+// streams of 16 dvec bytes).
 template <bool BWD, bool POST, bool S2>
 lemo_status run_norm(lemo::norm::Args& a, cudaStream_t st, int* grid) {
+    using lemo::norm::Shape;
     int dev = 0;
     const int sms = device_sms(&dev);
     if (sms <= 0) return LEMO_ERR_CUDA;
@@ -1233,14 +1236,14 @@ lemo_status run_norm(lemo::norm::Args& a, cudaStream_t st, int* grid) {
         a.spin_limit_ns = (uint64_t)g_spin_ns;
     }
     bool ok;
-    if (a.dvec <= 32) ok = launch_norm<BWD, POST, S2, 32, 1>(a, dev, sms, st, grid);
-    else if (a.dvec <= 64) ok = launch_norm<BWD, POST, S2, 32, 2>(a, dev, sms, st, grid);
-    else if (a.dvec <= 128) ok = launch_norm<BWD, POST, S2, 64, 2>(a, dev, sms, st, grid);
-    else if (a.dvec <= 256) ok = launch_norm<BWD, POST, S2, 128, 2>(a, dev, sms, st, grid);
-    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, S2, 256, 2>(a, dev, sms, st, grid);
-    else if (a.dvec <= 768) ok = launch_norm<BWD, POST, S2, 256, 3>(a, dev, sms, st, grid);
-    else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, S2, 512, 2>(a, dev, sms, st, grid);
-    else ok = launch_norm<BWD, POST, S2, 512, 4>(a, dev, sms, st, grid);
+    if (a.dvec <= 32) ok = launch_norm<BWD, POST, S2, Shape<32, 1, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 64) ok = launch_norm<BWD, POST, S2, Shape<64, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 128) ok = launch_norm<BWD, POST, S2, Shape<128, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 256) ok = launch_norm<BWD, POST, S2, Shape<256, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, S2, Shape<512, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 640) ok = launch_norm<BWD, POST, S2, Shape<640, 1, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, S2, Shape<512, 2, 2>>(a, dev, sms, st, grid);
+    else ok = launch_norm<BWD, POST, S2, Shape<512, 4, 1>>(a, dev, sms, st, grid);
     const lemo_status e = launch_status();
     return ok ? e : LEMO_ERR_CUDA;
 }

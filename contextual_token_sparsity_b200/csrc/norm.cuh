@@ -21,11 +21,12 @@
 // All rows are bf16; every kernel here is bound by HBM.  One CTA per SM takes
 // rows in a fixed order: a producer warp copies the rows that a stage needs
 // (cp.async.bulk, whole rows) into a ring in shared memory, up to ~200 KB in
-// flight per SM whatever the register use, and NG groups of G threads take one
-// row of each stage.  A thread owns the same V vectors of 8 columns in every
-// row, so weights stay in registers, column sums are per-thread registers, and a
-// row costs one or two reductions over its group.  The CTAs' column sums are
-// added by a second kernel in CTA order, so every result is deterministic.
+// flight per SM whatever the register use, and each of NG groups of G threads
+// takes R rows of a stage at once.  A thread owns the same V vectors of 8 columns in
+// every row, so weights stay in registers, column sums are per-thread registers,
+// and R rows share one reduction over the group (its latency, ~300 cycles, is what
+// a single row per turn was bound by).  The CTAs' column sums are added by a
+// second kernel in CTA order, so every result is deterministic.
 #pragma once
 
 #include "ckpt.cuh"
@@ -47,11 +48,22 @@ enum Kind : int { kNoNorm = 0, kRms = 1, kLayer = 2 };
 
 constexpr int kMaxParts = 296;  // CTAs that leave column sums in the workspace, at most
 constexpr int kMaxD = 16384;
-constexpr int kConsumers = 512; // threads that work on rows; one more warp copies them
-constexpr int kThreads = kConsumers + 32;
 constexpr int kMaxStages = 8;
-constexpr int kMaxGroups = kConsumers / 32;
+constexpr int kMaxRows = 32;    // rows of a stage: one per lane of the producer warp
+constexpr int kMaxWarps = 20;   // consumer warps
 constexpr int kMaxSmem = 220 * 1024;
+
+// G threads per group, V vectors per thread, R rows per group and stage.
+template <int G_, int V_, int R_>
+struct Shape {
+    static constexpr int G = G_, V = V_, R = R_;
+    static constexpr int kConsumers = G > 512 ? G : 512;
+    static constexpr int kThreads = kConsumers + 32;  // and the producer warp
+    static constexpr int kGroups = kConsumers / G;
+    static constexpr int kWarps = G / 32;
+    static constexpr int kRows = kGroups * R;         // rows of a stage
+    static_assert(kRows <= kMaxRows && kConsumers / 32 <= kMaxWarps, "");
+};
 
 struct Args {
     int kind;
@@ -94,12 +106,12 @@ struct Args {
 struct Smem {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
-    int64_t token[kMaxStages][kMaxGroups];  // -1: no row, or refused
-    float2 stats[kMaxStages][kMaxGroups];
-    float2 red[2][kConsumers / 32];  // one per consumer warp, two alternating buffers
+    int64_t token[kMaxStages][kMaxRows];  // -1: no row, or refused
+    float2 stats[kMaxStages][kMaxRows];
+    float red[2][kMaxWarps][8];           // per consumer warp, two alternating buffers
     int abort_flag;
 };
-constexpr int kRing = 3072;  // offset of the ring
+constexpr int kRing = 6144;  // offset of the ring
 static_assert(sizeof(Smem) <= kRing, "the ring starts behind the barriers");
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Smem* sm, uint64_t limit_ns) {
@@ -145,35 +157,48 @@ __device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
     return v;
 }
 
-template <int G>
-struct Shape {
-    static constexpr int kGroups = kConsumers / G;
-    static constexpr int kWarps = G / 32;
-};
-
-// Sums of two values over the G threads of a group, returned to all of them.
-// `red` holds two alternating buffers, so one barrier per call is enough.
-template <int G>
-__device__ __forceinline__ float2 group_sum(float a, float b, Smem* sm, int& flip) {
+// Sums of N values (a power of two, at most 8) over the threads of a group,
+// returned to all of them in p.  Inside a warp the values are folded onto lanes
+// (N - 1 shuffles instead of 5 N); `red` has two alternating buffers, so one
+// barrier per call is enough.
+template <typename S, int N>
+__device__ __forceinline__ void group_sum(float (&p)[N], Smem* sm, int& flip) {
+    const int lane = threadIdx.x & 31;
+    int m = 16, idx = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if constexpr (G == 32) {
-        return make_float2(a, b);
-    } else {
-        if ((threadIdx.x & 31) == 0) sm->red[flip][threadIdx.x >> 5] = make_float2(a, b);
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)(threadIdx.x / G)), "n"(G) : "memory");
-        a = b = 0.f;
+    for (int n = N; n > 1; n /= 2, m /= 2) {
+        const bool hi = lane & m;
+        idx += hi ? n / 2 : 0;
 #pragma unroll
-        for (int i = 0; i < Shape<G>::kWarps; ++i) {
-            const float2 p = sm->red[flip][threadIdx.x / G * Shape<G>::kWarps + i];
-            a += p.x;
-            b += p.y;
+        for (int i = 0; i < n / 2; ++i) {
+            const float send = hi ? p[i] : p[i + n / 2], keep = hi ? p[i + n / 2] : p[i];
+            p[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
+    }
+    const int low = m;  // lanes that differ below 2 m hold the same value
+#pragma unroll
+    for (; m > 0; m /= 2) p[0] += __shfl_xor_sync(0xffffffffu, p[0], m);
+    float total = p[0];  // of value idx
+    if constexpr (S::kWarps > 1) {
+        if ((lane & (2 * low - 1)) == 0) sm->red[flip][threadIdx.x >> 5][idx] = total;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)(threadIdx.x / S::G)), "n"(S::G) : "memory");
+        const int w0 = threadIdx.x / S::G * S::kWarps;
+        total = 0.f;
+        for (int w = lane / N; w < S::kWarps; w += 32 / N) total += sm->red[flip][w0 + w][lane % N];
+#pragma unroll
+        for (int o = N; o < 32; o *= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
         flip ^= 1;
-        return make_float2(a, b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = __shfl_sync(0xffffffffu, total, i);
+    } else {
+        // value i sits on the lane whose upper bits spell i, highest first
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int src = 0;
+#pragma unroll
+            for (int n = N, bit = 16; n > 1; n /= 2, bit /= 2) src |= (i & (n / 2)) ? bit : 0;
+            p[i] = __shfl_sync(0xffffffffu, total, src);
+        }
     }
 }
 
@@ -182,28 +207,28 @@ __device__ __forceinline__ uint4 ld_or(const uint4* p, int c, bool in, uint32_t 
 }
 constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 
-// Row of group g in stage st of this CTA.
-template <int G>
-__device__ __forceinline__ int64_t row_of(int64_t st, int g) {
-    return blockIdx.x + (st * Shape<G>::kGroups + g) * (int64_t)gridDim.x;
+// Row j of stage st of this CTA.
+template <typename S>
+__device__ __forceinline__ int64_t row_of(int64_t st, int j) {
+    return blockIdx.x + (st * S::kRows + j) * (int64_t)gridDim.x;
 }
 
-// The producer warp: lane g brings the row of group g.
-template <int G>
+// The producer warp: lane j brings row j of a stage.
+template <typename S>
 __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, int64_t K,
                                         bool ascending, bool want_stats) {
-    constexpr int NG = Shape<G>::kGroups;
+    constexpr int NR = S::kRows;
     const int lane = threadIdx.x & 31;
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
     int64_t st = 0;
-    for (; row_of<G>(st, 0) < K; ++st) {
-        // this stage's token and statistics, read while the slot may still be in use
-        const int64_t r = row_of<G>(st, lane);
+    for (; row_of<S>(st, 0) < K; ++st) {
+        // this stage's tokens and statistics, read while the slot may still be in use
+        const int64_t r = row_of<S>(st, lane);
         int64_t t = -1;
         float2 stat = make_float2(0.f, 1.f);
-        if (lane < NG && r < K) {
+        if (lane < NR && r < K) {
             t = a.kept_idx ? a.kept_idx[r] : r;
             bool good = t >= 0 && t < a.x_rows && t < a.src_rows;
             // two rows of one token would race in the kernels that update token rows
@@ -216,7 +241,7 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
         }
         if (!(ok = wait_warp(&sm->empty[s], ph ^ 1, sm, a.spin_limit_ns))) break;
         const uint32_t rows = __ballot_sync(0xffffffffu, t >= 0);
-        if (lane < NG) {
+        if (lane < NR) {
             sm->token[s][lane] = t;
             sm->stats[s][lane] = stat;
         }
@@ -228,7 +253,7 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
         }
         __syncwarp();
         if (t >= 0) {
-            const uint32_t dst = ring + (uint32_t)(s * NG + lane) * a.slot;
+            const uint32_t dst = ring + (uint32_t)(s * NR + lane) * a.slot;
             for (int i = 0; i < a.streams; ++i)
                 bulk_load(dst + a.in[i].off, a.in[i].base + (a.in[i].by_token ? t : r) * a.in[i].ld,
                           a.in[i].bytes, &sm->full[s]);
@@ -248,12 +273,12 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
     }
 }
 
-template <int G>
+template <typename S>
 __device__ __forceinline__ void init_ring(const Args& a, Smem* sm) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&sm->full[s], 1);
-            mbar_init(&sm->empty[s], kConsumers / 32);
+            mbar_init(&sm->empty[s], S::kConsumers / 32);
         }
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -262,31 +287,32 @@ __device__ __forceinline__ void init_ring(const Args& a, Smem* sm) {
 }
 
 // Zero rows [K, K_pad) of the kept-row output.
+template <typename S>
 __device__ __forceinline__ void zero_tail(const Args& a, int64_t K, int64_t K_pad) {
     const int64_t n = (K_pad - K) * a.dvec;
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * kThreads)
+    for (int64_t i = blockIdx.x * (int64_t)S::kThreads + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * S::kThreads)
         a.y[(K + i / a.dvec) * a.ld_y + i % a.dvec] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ---------------------------------------------------------------------------
 // Forward.  Streams: gather x; scatter y, x, (gate rows).
 // ---------------------------------------------------------------------------
-template <int G, int V, bool POST>
-__global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_constant__ Args a) {
+template <typename S, bool POST>
+__global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_constant__ Args a) {
+    constexpr int G = S::G, V = S::V, R = S::R;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem* sm = reinterpret_cast<Smem*>(smem_raw);
-    init_ring<G>(a, sm);
+    init_ring<S>(a, sm);
     pdl_entry();
-    constexpr int NG = Shape<G>::kGroups;
     const uint32_t ring = smem_u32(smem_raw) + kRing;
     const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
     if (!POST) {
         const int64_t K_pad = ckpt::clamp_pad(K, a.pad_to, a.rows);
-        if (K_pad > K) zero_tail(a, K, K_pad);
+        if (K_pad > K) zero_tail<S>(a, K, K_pad);
     }
-    if (threadIdx.x >= kConsumers) {
-        produce<G>(a, sm, ring, K, POST, false);
+    if (threadIdx.x >= S::kConsumers) {
+        produce<S>(a, sm, ring, K, POST, false);
         return;
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
@@ -301,59 +327,77 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     }
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t st = 0; row_of<G>(st, 0) < K; ++st) {
+    for (int64_t st = 0; row_of<S>(st, 0) < K; ++st) {
         if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
-        const int64_t t = sm->token[s][group];
-        if (t >= 0) {
-            const int64_t r = row_of<G>(st, group);
-            const uint32_t row = ring + (uint32_t)(s * NG + group) * a.slot;
-            uint4 in[V];
+        const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
+        const int64_t* token = &sm->token[s][group * R];
+        uint4 in[R][V];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
-                in[v] = c < a.dvec ? ld_shared(row + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+                in[q][v] = token[q] >= 0 && c < a.dvec ? ld_shared(row0 + q * a.slot + 16 * c)
+                                                       : make_uint4(0u, 0u, 0u, 0u);
             }
-            float mean = 0.f, rstd = 1.f;
-            if (a.kind != kNoNorm) {
-                if (a.kind == kLayer) {
-                    float sum = 0.f;
+        float mean[R], rstd[R];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float f[8];
-                        unpack8(in[v], f);
+        for (int q = 0; q < R; ++q) {
+            mean[q] = 0.f;
+            rstd[q] = 1.f;
+        }
+        if (a.kind == kLayer) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sum += f[j];
-                    }
-                    mean = group_sum<G>(sum, 0.f, sm, flip).x * a.inv_d;
-                }
-                float sum = 0.f;
+            for (int q = 0; q < R; ++q)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float f[8];
-                    unpack8(in[v], f);
+                    unpack8(in[q][v], f);
+                    mean[q] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                }
+            group_sum<S, R>(mean, sm, flip);
+#pragma unroll
+            for (int q = 0; q < R; ++q) mean[q] *= a.inv_d;
+        }
+        if (a.kind != kNoNorm) {
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                rstd[q] = 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float f[8];
+                    unpack8(in[q][v], f);
                     if (v * G + i < a.dvec) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sum += (f[j] - mean) * (f[j] - mean);
+                        for (int j = 0; j < 8; ++j) rstd[q] += (f[j] - mean[q]) * (f[j] - mean[q]);
                     }
                 }
-                rstd = 1.f / sqrtf(group_sum<G>(sum, 0.f, sm, flip).x * a.inv_d + a.eps);
             }
-            if (a.stats && i == 0) a.stats[r] = make_float2(mean, rstd);
+            group_sum<S, R>(rstd, sm, flip);
+#pragma unroll
+            for (int q = 0; q < R; ++q) rstd[q] = 1.f / sqrtf(rstd[q] * a.inv_d + a.eps);
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t t = token[q], r = row_of<S>(st, group * R + q);
+            if (t < 0) continue;
+            if (a.stats && i == 0) a.stats[r] = make_float2(mean[q], rstd[q]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
                 if (a.c.format >= 0) {
-                    const uint32_t code = ckpt::scale_code(in[v], a.c.format);
-                    if (c < a.dvec) ckpt::store8(a.c, r, c, in[v], code);
+                    const uint32_t code = ckpt::scale_code(in[q][v], a.c.format);
+                    if (c < a.dvec) ckpt::store8(a.c, r, c, in[q][v], code);
                 }
                 if (c >= a.dvec) continue;
                 float f[8], wf[8], bf[8];
-                unpack8(in[v], f);
+                unpack8(in[q][v], f);
                 unpack8(w[v], wf);
                 unpack8(b[v], bf);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd * wf[j] + bf[j];
+                for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean[q]) * rstd[q], wf[j], bf[j]);
                 if (POST) {
+                    const uint32_t row = row0 + q * a.slot;
                     float gf[8], xf[8];
                     unpack8(a.streams == 3 ? ld_shared(row + a.in[2].off + 16 * c) : gate[v], gf);
                     unpack8(ld_shared(row + a.in[1].off + 16 * c), xf);
@@ -378,21 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
 // Backward.  Streams: the normalised row (bf16 or codes); gather dy, dx;
 // scatter dx, (gate rows).  S2: the sums of dy (dn) are wanted too.
 // ---------------------------------------------------------------------------
-template <int G, int V, bool POST, bool S2>
-__global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_constant__ Args a) {
+template <typename S, bool POST, bool S2>
+__global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_constant__ Args a) {
+    constexpr int G = S::G, V = S::V, R = S::R, NG = S::kGroups;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem* sm = reinterpret_cast<Smem*>(smem_raw);
-    init_ring<G>(a, sm);
+    init_ring<S>(a, sm);
     pdl_entry();
-    constexpr int NG = Shape<G>::kGroups;
     const uint32_t ring = smem_u32(smem_raw) + kRing;
     const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
     if (POST) {
         const int64_t K_pad = ckpt::clamp_pad(K, a.pad_to, a.rows);
-        if (K_pad > K) zero_tail(a, K, K_pad);
+        if (K_pad > K) zero_tail<S>(a, K, K_pad);
     }
-    if (threadIdx.x >= kConsumers) {
-        produce<G>(a, sm, ring, K, !POST, a.kind != kNoNorm);
+    if (threadIdx.x >= S::kConsumers) {
+        produce<S>(a, sm, ring, K, !POST, a.kind != kNoNorm);
         return;
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
@@ -407,70 +451,79 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         s1[j] = 0.f;
         if (S2) s2[j] = 0.f;
     }
-    // scale bytes of this group's next row
-    uint32_t code[V];
-    auto load_codes = [&](int64_t r) {
-        if (!coded || r >= K) return;
+    // scale bytes of this group's next rows
+    uint32_t code[R][V];
+    auto load_codes = [&](int64_t st) {
+        if (!coded) return;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * G + i;
-            code[v] = c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
-        }
-    };
-    load_codes(row_of<G>(0, group));
-    int s = 0;
-    uint32_t ph = 0;
-    for (int64_t st = 0; row_of<G>(st, 0) < K; ++st) {
-        if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
-        const int64_t t = sm->token[s][group];
-        const int64_t r = row_of<G>(st, group);
-        if (t >= 0) {
-            const uint32_t row = ring + (uint32_t)(s * NG + group) * a.slot;
-            const float2 stat = sm->stats[s][group];
-            const float mean = stat.x, rstd = stat.y;
-            // The row's raw vectors stay in registers over the reduction, not what they unpack
-            // to (a third of the registers); both passes unpack them.
-            uint4 raw_v[V], raw_g[V];
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = row_of<S>(st, group * R + q);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
-                raw_v[v] = raw_g[v] = make_uint4(0u, 0u, 0u, 0u);
-                if (c >= a.dvec) continue;
-                if (coded) {
-                    const uint2 q = ld_shared8(row + 8 * c);
-                    raw_v[v].x = q.x;
-                    raw_v[v].y = q.y;
-                } else {
-                    raw_v[v] = ld_shared(row + 16 * c);
-                }
-                raw_g[v] = ld_shared(row + a.in[1].off + 16 * c);
+                code[q][v] = r < K && c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
             }
-            auto vhat = [&](int v, float* f) {
-                if (coded)
-                    ckpt::decode8(make_uint2(raw_v[v].x, raw_v[v].y), code[v], a.c.format, f);
-                else
-                    unpack8(raw_v[v], f);
+        }
+    };
+    load_codes(0);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int64_t st = 0; row_of<S>(st, 0) < K; ++st) {
+        if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
+        const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
+        const int64_t* token = &sm->token[s][group * R];
+        const float2* stats = &sm->stats[s][group * R];
+        // The rows' raw vectors stay in registers over the reduction, not what they unpack to
+        // (a third of the registers); both passes unpack them.
+        uint4 raw_v[R][V], raw_g[R][V];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd;
-            };
-            // gate of vector v (POST)
-            auto gated = [&](int v, float* gf) {
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
-                unpack8(a.ld_gate ? ld_shared(row + a.in[2].off + 16 * c) : ld_or(a.gate, c, true, kOnes),
-                        gf);
-            };
-            float p1 = 0.f, p2 = 0.f;
+                const uint32_t row = row0 + q * a.slot;
+                raw_v[q][v] = raw_g[q][v] = make_uint4(0u, 0u, 0u, 0u);
+                if (token[q] < 0 || c >= a.dvec) continue;
+                if (coded) {
+                    const uint2 k = ld_shared8(row + 8 * c);
+                    raw_v[q][v].x = k.x;
+                    raw_v[q][v].y = k.y;
+                } else {
+                    raw_v[q][v] = ld_shared(row + 16 * c);
+                }
+                raw_g[q][v] = ld_shared(row + a.in[1].off + 16 * c);
+            }
+        auto vhat = [&](int q, int v, float* f) {
+            const float2 m = stats[q];  // (mean, rstd)
+            if (coded)
+                ckpt::decode8(make_uint2(raw_v[q][v].x, raw_v[q][v].y), code[q][v], a.c.format, f);
+            else
+                unpack8(raw_v[q][v], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = (f[j] - m.x) * m.y;  // no cancellation next to the mean
+        };
+        // gate of vector v (POST)
+        auto gated = [&](int q, int v, float* gf) {
+            const int c = v * G + i;
+            unpack8(a.ld_gate ? ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c)
+                              : ld_or(a.gate, c, true, kOnes), gf);
+        };
+        float p[2 * R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            p[q] = p[R + q] = 0.f;
+            if (token[q] < 0) continue;  // no row: nothing goes into the sums
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
                 if (c >= a.dvec) continue;
                 float vv[8], gg[8], wf[8];
-                vhat(v, vv);
-                unpack8(raw_g[v], gg);
+                vhat(q, v, vv);
+                unpack8(raw_g[q][v], gg);
                 unpack8(w[v], wf);
                 if (POST) {
                     float gf[8];
-                    gated(v, gf);
+                    gated(q, v, gf);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) gg[j] *= a.scale;
                     if (a.dgate_rows) {
@@ -478,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                         unpack8(ld_or(a.b, c, true, 0u), bf);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) bf[j] = gg[j] * (vv[j] * wf[j] + bf[j]);
-                        a.dgate_rows[r * a.ld_dgate + c] = pack8(bf);
+                        a.dgate_rows[row_of<S>(st, group * R + q) * a.ld_dgate + c] = pack8(bf);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -498,40 +551,52 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     gg[j] *= wf[j];
-                    p1 += gg[j] * vv[j];
-                    p2 += gg[j];
+                    p[q] += gg[j] * vv[j];
+                    p[R + q] += gg[j];
                 }
             }
-            float c1 = 0.f, c2 = 0.f;
-            if (a.kind != kNoNorm) {
-                const float2 p = group_sum<G>(p1, p2, sm, flip);
-                c1 = p.x * a.inv_d;
-                c2 = a.kind == kLayer ? p.y * a.inv_d : 0.f;
+        }
+        if (a.kind != kNoNorm) {
+            group_sum<S, 2 * R>(p, sm, flip);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                p[q] *= a.inv_d;
+                p[R + q] = a.kind == kLayer ? p[R + q] * a.inv_d : 0.f;
             }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2 * R; ++q) p[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t t = token[q], r = row_of<S>(st, group * R + q);
+            if (t < 0) continue;
+            const float rstd = stats[q].y;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
                 if (c >= a.dvec) continue;
                 // opaque: or the compiler keeps the unpacked values of the first pass instead
-                asm volatile("" : "+r"(raw_v[v].x), "+r"(raw_v[v].y), "+r"(raw_v[v].z), "+r"(raw_v[v].w),
-                             "+r"(raw_g[v].x), "+r"(raw_g[v].y), "+r"(raw_g[v].z), "+r"(raw_g[v].w));
+                asm volatile("" : "+r"(raw_v[q][v].x), "+r"(raw_v[q][v].y), "+r"(raw_v[q][v].z),
+                             "+r"(raw_v[q][v].w), "+r"(raw_g[q][v].x), "+r"(raw_g[q][v].y),
+                             "+r"(raw_g[q][v].z), "+r"(raw_g[q][v].w));
                 float vv[8], gg[8], wf[8];
-                vhat(v, vv);
-                unpack8(raw_g[v], gg);
+                vhat(q, v, vv);
+                unpack8(raw_g[q][v], gg);
                 unpack8(w[v], wf);
                 if (POST) {
                     float gf[8];
-                    gated(v, gf);
+                    gated(q, v, gf);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) gg[j] = gg[j] * a.scale * gf[j];
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) gg[j] = rstd * (gg[j] * wf[j] - vv[j] * c1 - c2);
+                for (int j = 0; j < 8; ++j) gg[j] = rstd * (gg[j] * wf[j] - vv[j] * p[q] - p[R + q]);
                 if (POST) {
                     a.y[r * a.ld_y + c] = pack8(gg);
                 } else {
                     float xf[8];
-                    unpack8(ld_shared(row + a.in[2].off + 16 * c), xf);
+                    unpack8(ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c), xf);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) gg[j] += xf[j];
                     a.x[t * a.ld_x + c] = pack8(gg);
@@ -540,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         }
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->empty[s]);
-        load_codes(row_of<G>(st + 1, group));
+        load_codes(st + 1);
         if (++s == a.stages) {
             s = 0;
             ph ^= 1;
@@ -551,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     if constexpr (NG > 1) {
         float* acc = reinterpret_cast<float*>(smem_raw + kRing);
         for (int gi = 0; gi < NG; ++gi) {
-            asm volatile("bar.sync 15, %0;" ::"n"(kConsumers) : "memory");
+            asm volatile("bar.sync 15, %0;" ::"n"(S::kConsumers) : "memory");
             if (gi == group) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -608,13 +673,15 @@ struct SumArgs {
     float* dgate;
 };
 
-constexpr int kSumCols = 32, kSumSlices = 16;
+constexpr int kSumCols = 32, kSumSlices = 32, kSumBatch = 5;
 
 __device__ __forceinline__ float bf(const uint16_t* p, int c, float other) {
     return p ? __uint_as_float((uint32_t)p[c] << 16) : other;
 }
 
-// Adds the CTAs' column sums in CTA order within 16 slices, then the slices in order.
+// Adds the CTAs' column sums in CTA order within 32 slices, then the slices in
+// order.  A thread's loads are issued kSumBatch rows at a time: 148 CTAs are one
+// batch per thread, so the kernel is one memory latency long, not five.
 __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sums_kernel(const SumArgs a) {
     pdl_entry();
     __shared__ float2 acc[kSumSlices][kSumCols];
@@ -626,10 +693,20 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sums_kernel(cons
     const int c = blockIdx.x * kSumCols + col;
     float2 s = make_float2(0.f, 0.f);
     if (c < a.d) {
-        for (int p = slice; p < parts; p += kSumSlices) {
-            const float* row = a.part + (int64_t)p * 2 * a.d;
-            s.x += row[c];
-            if (a.second) s.y += row[a.d + c];
+        for (int p0 = slice; p0 < parts; p0 += kSumSlices * kSumBatch) {
+            float x[kSumBatch], y[kSumBatch];
+#pragma unroll
+            for (int j = 0; j < kSumBatch; ++j) {
+                const int p = p0 + j * kSumSlices;
+                const float* row = a.part + (int64_t)p * 2 * a.d;
+                x[j] = p < parts ? row[c] : 0.f;
+                y[j] = p < parts && a.second ? row[a.d + c] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kSumBatch; ++j) {
+                s.x += x[j];
+                s.y += y[j];
+            }
         }
     }
     acc[slice][col] = s;
