@@ -16,7 +16,10 @@
 //
 // Four neighbouring lanes hold one group (8 bf16 each in one 16-byte vector),
 // so its maximum costs two shuffles on packed 16-bit magnitudes (bf16
-// magnitudes order like integers).
+// magnitudes order like integers).  The kernels are bound by HBM, with the issue
+// slots next: values are taken as packed fp32 pairs throughout, the scale byte is
+// one add and one shift of the magnitude, and the rare cases (infinities, NaN, the
+// largest scale) share one branch.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,113 +47,157 @@ struct View {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ void unpack8(uint4 v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf_lo(w[i]);
-        f[2 * i + 1] = bf_hi(w[i]);
-    }
+// Two fp32 values worked on by one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unf2(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 two(float x) { return f2(x, x); }
+
+// The eight bf16 values of a vector as four fp32 pairs, and back.
+__device__ __forceinline__ void unpack8(uint4 v, F2* f) {
+    f[0] = f2(bf_lo(v.x), bf_hi(v.x));
+    f[1] = f2(bf_lo(v.y), bf_hi(v.y));
+    f[2] = f2(bf_lo(v.z), bf_hi(v.z));
+    f[3] = f2(bf_lo(v.w), bf_hi(v.w));
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+    const float2 f = unf2(a);
+    return pack2(f.x, f.y);
+}
+__device__ __forceinline__ uint4 pack8(const F2* f) {
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
 
 // Scale byte of the group of four lanes that this lane belongs to, from the
 // lane's 8 values (zeros where it has none).  Called by whole warps.
+// magnitude = 1.man 2^(exp - 127); 448 = (1 + 96/128) 2^8, 127 = (1 + 126/128) 2^6:
+// the byte is exp - 8 or exp - 6, one more where man is above 96 or 126.
 __device__ __forceinline__ uint32_t scale_code(uint4 v, int format) {
     constexpr uint32_t kMag = 0x7fff7fffu;
     uint32_t m = __vmaxu2(__vmaxu2(v.x & kMag, v.y & kMag), __vmaxu2(v.z & kMag, v.w & kMag));
     m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t mag = max(m & 0xffffu, m >> 16);
-    if (mag >= 0x7f80u) return 255u;
-    // magnitude = 1.man 2^(exp - 127); 448 = 1.75 2^8, 127 = (1 + 126/128) 2^6
-    const int exp = (int)(mag >> 7), man = (int)(mag & 127u);
-    const int code = format == kE4M3 ? exp - 8 + (man > 96) : exp - 6 + (man > 126);
-    return (uint32_t)max(code, kMinCode);
+    const int mag = (int)max(m & 0xffffu, m >> 16);
+    const int code = format == kE4M3 ? ((mag + 31) >> 7) - 8 : ((mag + 1) >> 7) - 6;
+    return mag >= 0x7f80 ? 255u : (uint32_t)max(code, kMinCode);
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t e4m3x4(F2 a, F2 b) {
+    const float2 x = unf2(a), y = unf2(b);
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.y), "f"(x.x));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y.y), "f"(y.x));
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// rne(t) for |t| <= 127 as the low byte of t + 1.5 2^23.
-__device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
-    constexpr float kMagic = 12582912.f;
-    const uint32_t x = __float_as_uint(a + kMagic), y = __float_as_uint(b + kMagic);
-    const uint32_t z = __float_as_uint(c + kMagic), w = __float_as_uint(d + kMagic);
-    return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+// Low bytes of the four floats: rne(t) for |t| <= 127 where they are t + 1.5 2^23.
+constexpr float kMagic = 12582912.f;
+__device__ __forceinline__ uint32_t low_bytes(F2 a, F2 b) {
+    const float2 x = unf2(a), y = unf2(b);
+    return __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                       __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
 }
 
-// Codes of 8 values under the group's scale byte.
-__device__ __forceinline__ uint2 encode8(uint4 v, uint32_t code, int format) {
+// Scale bytes from here on are rare: the one of each format under which a
+// magnitude next to 2^128 could round up to 2^128 (247, 249), and 255.
+constexpr uint32_t kRareCode = 247;
+
+__device__ __noinline__ uint2 encode8_rare(uint4 v, uint32_t code, int format) {
     if (code == 255u) {
         const uint32_t q = format == kE4M3 ? 0x7f7f7f7fu : 0u;
         return make_uint2(q, q);
     }
     const float inv = __uint_as_float((254u - code) << 23);  // 2^-k
-    float f[8];
+    const float most = code != (format == kE4M3 ? 247u : 249u) ? 448.f : format == kE4M3 ? 240.f : 63.f;
+    F2 f[4];
     unpack8(v, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= inv;
-    // the one scale of each format under which a magnitude next to 2^128 could round up to 2^128
-    const float most = format == kE4M3 ? 240.f : 63.f;
-    if (code == (format == kE4M3 ? 247u : 249u)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -most), most);
+    for (int i = 0; i < 4; ++i) {
+        float2 t = unf2(f[i]);
+        t.x = fminf(fmaxf(t.x * inv, -most), most);
+        t.y = fminf(fmaxf(t.y * inv, -most), most);
+        f[i] = format == kE4M3 ? f2(t.x, t.y) : f2(t.x + kMagic, t.y + kMagic);
     }
-    if (format == kE4M3)
-        return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-    return make_uint2(int8x4(f[0], f[1], f[2], f[3]), int8x4(f[4], f[5], f[6], f[7]));
+    return format == kE4M3 ? make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]))
+                           : make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
 }
 
-__device__ __forceinline__ void decode4(uint32_t q, float s, int format, float* f) {
+// Codes of 8 values under the group's scale byte.
+__device__ __forceinline__ uint2 encode8(uint4 v, uint32_t code, int format) {
+    if (code >= kRareCode) return encode8_rare(v, code, format);
+    const F2 inv = two(__uint_as_float((254u - code) << 23));  // 2^-k
+    F2 f[4];
+    unpack8(v, f);
+    if (format == kE4M3) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], inv);
+        return make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = fma2(f[i], inv, two(kMagic));
+    return make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
+}
+
+__device__ __forceinline__ void decode4(uint32_t q, F2 s, int format, F2* f) {
     if (format == kE4M3) {
         uint32_t h0, h1;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)(q & 0xffffu)));
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(q >> 16)));
         const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-        f[0] = a.x * s;
-        f[1] = a.y * s;
-        f[2] = b.x * s;
-        f[3] = b.y * s;
+        f[0] = mul2(f2(a.x, a.y), s);
+        f[1] = mul2(f2(b.x, b.y), s);
     } else {
         // q ^ 0x80 = value + 128 as an unsigned byte; 2^23 + that, minus both offsets
         const uint32_t u = q ^ 0x80808080u;
-        constexpr float kBias = 8388608.f + 128.f;
-        f[0] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - kBias) * s;
-        f[1] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - kBias) * s;
-        f[2] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - kBias) * s;
-        f[3] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - kBias) * s;
+        const F2 bias = two(-8388736.f);
+        f[0] = mul2(add2(f2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)),
+                            __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441))), bias), s);
+        f[1] = mul2(add2(f2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)),
+                            __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443))), bias), s);
     }
 }
 
 // The 8 values (exact in bf16) of two words of codes.
-__device__ __forceinline__ void decode8(uint2 q, uint32_t code, int format, float* f) {
-    const float s = code == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(code << 23);
+__device__ __forceinline__ void decode8(uint2 q, uint32_t code, int format, F2* f) {
+    const F2 s = two(code == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(code << 23));
     decode4(q.x, s, format, f);
-    decode4(q.y, s, format, f + 4);
+    decode4(q.y, s, format, f + 2);
 }
 
 __device__ __forceinline__ void store8(const View& c, int64_t r, int vec, uint4 v, uint32_t code) {
     *reinterpret_cast<uint2*>(c.data + r * c.ld + 8 * (int64_t)vec) = encode8(v, code, c.format);
     if ((vec & 3) == 0) c.scales[r * c.ld_scales + (vec >> 2)] = (uint8_t)code;
-}
-
-__device__ __forceinline__ void load8(const View& c, int64_t r, int vec, float* f) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(c.data + r * c.ld + 8 * (int64_t)vec));
-    decode8(q, __ldg(c.scales + r * c.ld_scales + (vec >> 2)), c.format, f);
 }
 
 // Rows that exist on the device: kept_total clamped to the buffers' rows.
@@ -187,8 +234,9 @@ struct RowsArgs {
 };
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 8;  // vectors per lane in flight
 
-// One warp per row, 32 vectors (8 groups) at a time.
+// One warp per row, 256 vectors (64 groups) at a time.
 __global__ void __launch_bounds__(kThreads) save_kernel(const RowsArgs a) {
     pdl_entry();
     const int64_t K = clamp_rows(a.kept_total, a.rows);
@@ -201,11 +249,20 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const RowsArgs a) {
             continue;
         }
         const uint4* src = a.x + t * a.ld;
-        for (int c0 = 0; c0 < a.dvec; c0 += 32) {
-            const int c = c0 + lane;
-            const uint4 v = c < a.dvec ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t code = scale_code(v, a.c.format);
-            if (c < a.dvec) store8(a.c, r, c, v, code);
+        for (int c0 = 0; c0 < a.dvec; c0 += 32 * kUnroll) {
+            uint4 v[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int c = c0 + 32 * u + lane;
+                v[u] = c < a.dvec ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int c = c0 + 32 * u + lane;
+                if (c0 + 32 * u >= a.dvec) break;  // warp-uniform
+                const uint32_t code = scale_code(v[u], a.c.format);
+                if (c < a.dvec) store8(a.c, r, c, v[u], code);
+            }
         }
     }
 }
@@ -218,14 +275,29 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const RowsArgs a) {
     const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
     for (int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; r < K_pad; r += nwarps) {
         uint4* dst = a.y + r * a.ld;
-        for (int c = lane; c < a.dvec; c += 32) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < K) {
-                float f[8];
-                load8(a.c, r, c, f);
-                v = pack8(f);
+        if (r >= K) {
+            for (int c = lane; c < a.dvec; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        const uint2* data = reinterpret_cast<const uint2*>(a.c.data + r * a.c.ld);
+        const uint8_t* scales = a.c.scales + r * a.c.ld_scales;
+        for (int c0 = 0; c0 < a.dvec; c0 += 32 * kUnroll) {
+            uint2 q[kUnroll];
+            uint32_t code[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int c = c0 + 32 * u + lane;
+                q[u] = c < a.dvec ? __ldg(data + c) : make_uint2(0u, 0u);
+                code[u] = c < a.dvec ? __ldg(scales + (c >> 2)) : 127u;
             }
-            dst[c] = v;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int c = c0 + 32 * u + lane;
+                if (c >= a.dvec) continue;
+                F2 f[4];
+                decode8(q[u], code[u], a.c.format, f);
+                dst[c] = pack8(f);
+            }
         }
     }
 }
@@ -260,73 +332,112 @@ __device__ __forceinline__ float sigmoid(float g) {
     const float t = __expf(-fabsf(g));
     return __fdividef(g >= 0.f ? 1.f : t, 1.f + t);
 }
+__device__ __forceinline__ F2 sigmoid2(F2 g) {
+    const float2 v = unf2(g);
+    return f2(sigmoid(v.x), sigmoid(v.y));
+}
 
-__global__ void __launch_bounds__(kThreads) gated_kernel(const GatedArgs p) {
+// A warp takes 32 vectors of a row at a time, kPairs of them in flight.
+constexpr int kPairs = 2;
+
+__global__ void __launch_bounds__(kThreads, 4) gated_kernel(const GatedArgs p) {
     pdl_entry();
     const int64_t K = clamp_rows(p.kept_total, p.rows);
     const int64_t K_pad = clamp_pad(K, p.pad_to, p.rows);
     const int lane = threadIdx.x & 31;
     const int chunks = (p.dvec + 31) / 32;
-    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-    for (int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w < K_pad * chunks;
-         w += nwarps) {
-        const int64_t r = w / chunks;
-        const int c = (int)(w - r * chunks) * 32 + lane;
-        const bool in = c < p.dvec;
-        uint4 out = make_uint4(0u, 0u, 0u, 0u);
-        if (r < K) {
-            const uint4 g = in ? __ldg(p.g + r * p.ld_g + c) : out;
-            const uint4 u = in ? __ldg(p.u + r * p.ld_u + c) : out;
-            if (p.cg.format >= 0) {
-                const uint32_t code = scale_code(g, p.cg.format);
-                if (in) store8(p.cg, r, c, g, code);
-            }
-            if (p.cu.format >= 0) {
-                const uint32_t code = scale_code(u, p.cu.format);
-                if (in) store8(p.cu, r, c, u, code);
-            }
-            float gf[8], uf[8];
-            unpack8(g, gf);
-            unpack8(u, uf);
+    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5, items = K_pad * chunks;
+    for (int64_t w0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w0 < items;
+         w0 += kPairs * nwarps) {
+        int64_t r[kPairs];
+        int c[kPairs];
+        uint4 g[kPairs], u[kPairs];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) gf[i] = gf[i] * sigmoid(gf[i]) * uf[i];
-            out = pack8(gf);
+        for (int k = 0; k < kPairs; ++k) {
+            const int64_t w = w0 + k * nwarps;
+            r[k] = w < items ? w / chunks : K_pad;
+            c[k] = (int)(w - r[k] * chunks) * 32 + lane;
+            g[k] = u[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (r[k] < K && c[k] < p.dvec) {
+                g[k] = __ldg(p.g + r[k] * p.ld_g + c[k]);
+                u[k] = __ldg(p.u + r[k] * p.ld_u + c[k]);
+            }
         }
-        if (in) p.a[r * p.ld_a + c] = out;
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            if (r[k] >= K_pad) break;
+            const bool in = c[k] < p.dvec;
+            if (r[k] < K) {
+                if (p.cg.format >= 0) {
+                    const uint32_t code = scale_code(g[k], p.cg.format);
+                    if (in) store8(p.cg, r[k], c[k], g[k], code);
+                }
+                if (p.cu.format >= 0) {
+                    const uint32_t code = scale_code(u[k], p.cu.format);
+                    if (in) store8(p.cu, r[k], c[k], u[k], code);
+                }
+            }
+            F2 gf[4], uf[4];  // a row of the tail: zeros, SiLU(0) 0 = 0
+            unpack8(g[k], gf);
+            unpack8(u[k], uf);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) gf[i] = mul2(mul2(gf[i], sigmoid2(gf[i])), uf[i]);
+            if (in) p.a[r[k] * p.ld_a + c[k]] = pack8(gf);
+        }
     }
 }
 
-__global__ void __launch_bounds__(kThreads) gated_backward_kernel(const GatedArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) gated_backward_kernel(const GatedArgs p) {
     pdl_entry();
     const int64_t K = clamp_rows(p.kept_total, p.rows);
     const int64_t K_pad = clamp_pad(K, p.pad_to, p.rows);
     const int lane = threadIdx.x & 31;
     const int chunks = (p.dvec + 31) / 32;
-    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
-    for (int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w < K_pad * chunks;
-         w += nwarps) {
-        const int64_t r = w / chunks;
-        const int c = (int)(w - r * chunks) * 32 + lane;
-        if (c >= p.dvec) continue;
-        float dg[8], du[8], act[8];
+    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5, items = K_pad * chunks;
+    for (int64_t w0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w0 < items;
+         w0 += kPairs * nwarps) {
+        int64_t r[kPairs];
+        int c[kPairs];
+        uint4 da[kPairs];
+        uint2 qg[kPairs], qu[kPairs];
+        uint32_t sg[kPairs], su[kPairs];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[i] = du[i] = act[i] = 0.f;
-        if (r < K) {
-            float g[8], u[8], da[8];
-            unpack8(__ldg(p.da + r * p.ld_da + c), da);
-            load8(p.cg, r, c, g);
-            load8(p.cu, r, c, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = sigmoid(g[i]), gs = g[i] * s;
-                act[i] = gs * u[i];
-                du[i] = da[i] * gs;
-                dg[i] = da[i] * u[i] * (s + gs * (1.f - s));
+        for (int k = 0; k < kPairs; ++k) {
+            const int64_t w = w0 + k * nwarps;
+            r[k] = w < items ? w / chunks : K_pad;
+            c[k] = (int)(w - r[k] * chunks) * 32 + lane;
+            da[k] = make_uint4(0u, 0u, 0u, 0u);
+            qg[k] = qu[k] = make_uint2(0u, 0u);  // a row of the tail: zeros
+            sg[k] = su[k] = 127u;
+            if (r[k] < K && c[k] < p.dvec) {
+                da[k] = __ldg(p.da + r[k] * p.ld_da + c[k]);
+                qg[k] = __ldg(reinterpret_cast<const uint2*>(p.cg.data + r[k] * p.cg.ld) + c[k]);
+                qu[k] = __ldg(reinterpret_cast<const uint2*>(p.cu.data + r[k] * p.cu.ld) + c[k]);
+                sg[k] = __ldg(p.cg.scales + r[k] * p.cg.ld_scales + (c[k] >> 2));
+                su[k] = __ldg(p.cu.scales + r[k] * p.cu.ld_scales + (c[k] >> 2));
             }
         }
-        p.dg[r * p.ld_dg + c] = pack8(dg);
-        p.du[r * p.ld_du + c] = pack8(du);
-        if (p.a) p.a[r * p.ld_a + c] = pack8(act);
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            if (r[k] >= K_pad || c[k] >= p.dvec) continue;
+            F2 g[4], u[4], d[4], act[4];
+            decode8(qg[k], sg[k], p.cg.format, g);  // code 0 is value 0 in both formats
+            decode8(qu[k], su[k], p.cu.format, u);
+            unpack8(da[k], d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 s = sigmoid2(g[i]), gs = mul2(g[i], s);
+                act[i] = mul2(gs, u[i]);
+                // s + g s (1 - s)
+                const F2 slope = fma2(gs, add2(two(1.f), mul2(s, two(-1.f))), s);
+                const F2 du = mul2(d[i], gs);
+                g[i] = mul2(mul2(d[i], u[i]), slope);
+                u[i] = du;
+            }
+            p.dg[r[k] * p.ld_dg + c[k]] = pack8(g);
+            p.du[r[k] * p.ld_du + c[k]] = pack8(u);
+            if (p.a) p.a[r[k] * p.ld_a + c[k]] = pack8(act);
+        }
     }
 }
 

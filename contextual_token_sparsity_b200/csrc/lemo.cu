@@ -1240,7 +1240,7 @@ lemo_status run_norm(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     else if (a.dvec <= 64) ok = launch_norm<BWD, POST, S2, Shape<64, 1, 4>>(a, dev, sms, st, grid);
     else if (a.dvec <= 128) ok = launch_norm<BWD, POST, S2, Shape<128, 1, 4>>(a, dev, sms, st, grid);
     else if (a.dvec <= 256) ok = launch_norm<BWD, POST, S2, Shape<256, 1, 4>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, S2, Shape<512, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, S2, Shape<256, 2, 2>>(a, dev, sms, st, grid);
     else if (a.dvec <= 640) ok = launch_norm<BWD, POST, S2, Shape<640, 1, 2>>(a, dev, sms, st, grid);
     else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, S2, Shape<512, 2, 2>>(a, dev, sms, st, grid);
     else ok = launch_norm<BWD, POST, S2, Shape<512, 4, 1>>(a, dev, sms, st, grid);
@@ -1324,13 +1324,26 @@ int wgrad_pairs(int dev, int sms, int format, Kernel kernel) {
     return pairs;
 }
 
-// Persistent grid of the element-wise checkpoint kernels.
-template <typename Kernel>
-int ckpt_grid(Kernel, int sms, int64_t warps) {
+// Persistent grid of the element-wise checkpoint kernels: one CTA per kThreads / 32
+// warps of work, at most as many as are resident at once.
+template <auto Kernel>
+int ckpt_grid(int dev, int sms, int64_t warps) {
+    static int per_sm[kMaxDevices];  // of this kernel
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (per_sm[dev] == 0) {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, lemo::ckpt::kThreads, 0) !=
+                cudaSuccess ||
+            n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        per_sm[dev] = n;
+    }
     const int64_t per = lemo::ckpt::kThreads / 32;
     int64_t grid = (warps + per - 1) / per;
     if (grid < 1) grid = 1;
-    const int64_t most = (int64_t)sms * 8;
+    const int64_t most = (int64_t)sms * per_sm[dev];
     return (int)(grid < most ? grid : most);
 }
 
@@ -1526,7 +1539,7 @@ lemo_status lemo_checkpoint_save(const uint16_t* x, int64_t ld_x, int64_t x_rows
     a.kept_total = kept_total;
     a.rows = checkpoint->rows;
     a.c = view_of(checkpoint);
-    launch(lemo::ckpt::save_kernel, ckpt_grid(lemo::ckpt::save_kernel, sms, a.rows),
+    launch(lemo::ckpt::save_kernel, ckpt_grid<lemo::ckpt::save_kernel>(dev, sms, a.rows),
            lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
     return launch_status();
 }
@@ -1551,7 +1564,7 @@ lemo_status lemo_checkpoint_restore(const lemo_checkpoint* checkpoint, const int
     a.rows = rows;
     a.pad_to = pad_to;
     a.c = view_of(checkpoint);
-    launch(lemo::ckpt::restore_kernel, ckpt_grid(lemo::ckpt::restore_kernel, sms, rows),
+    launch(lemo::ckpt::restore_kernel, ckpt_grid<lemo::ckpt::restore_kernel>(dev, sms, rows),
            lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
     return launch_status();
 }
@@ -1584,7 +1597,7 @@ lemo_status lemo_gated_mlp(const uint16_t* gate, int64_t ld_gate, const uint16_t
     a.cg = view_of(gate_checkpoint);
     a.cu = view_of(up_checkpoint);
     launch(lemo::ckpt::gated_kernel,
-           ckpt_grid(lemo::ckpt::gated_kernel, sms, rows * ((a.dvec + 31) / 32)),
+           ckpt_grid<lemo::ckpt::gated_kernel>(dev, sms, rows * ((a.dvec + 31) / 32)),
            lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
     return launch_status();
 }
@@ -1623,7 +1636,7 @@ lemo_status lemo_gated_mlp_backward(const lemo_checkpoint* gate_checkpoint,
     a.cg = view_of(gate_checkpoint);
     a.cu = view_of(up_checkpoint);
     launch(lemo::ckpt::gated_backward_kernel,
-           ckpt_grid(lemo::ckpt::gated_backward_kernel, sms, rows * ((a.dvec + 31) / 32)),
+           ckpt_grid<lemo::ckpt::gated_backward_kernel>(dev, sms, rows * ((a.dvec + 31) / 32)),
            lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
     return launch_status();
 }

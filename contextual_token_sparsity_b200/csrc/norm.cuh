@@ -36,7 +36,13 @@
 namespace lemo {
 namespace norm {
 
+using ckpt::add2;
+using ckpt::F2;
+using ckpt::fma2;
+using ckpt::mul2;
 using ckpt::pack8;
+using ckpt::two;
+using ckpt::unf2;
 using ckpt::unpack8;
 using score::mbar_arrive;
 using score::mbar_arrive_expect_tx;
@@ -348,13 +354,16 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
         }
         if (a.kind == kLayer) {
 #pragma unroll
-            for (int q = 0; q < R; ++q)
+            for (int q = 0; q < R; ++q) {
+                F2 sum = two(0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float f[8];
+                    F2 f[4];
                     unpack8(in[q][v], f);
-                    mean[q] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                    sum = add2(sum, add2(add2(f[0], f[1]), add2(f[2], f[3])));
                 }
+                mean[q] = unf2(sum).x + unf2(sum).y;
+            }
             group_sum<S, R>(mean, sm, flip);
 #pragma unroll
             for (int q = 0; q < R; ++q) mean[q] *= a.inv_d;
@@ -362,47 +371,57 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
         if (a.kind != kNoNorm) {
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                rstd[q] = 0.f;
+                const F2 minus = two(-mean[q]);
+                F2 sum = two(0.f), sum2 = two(0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float f[8];
+                    if (v * G + i >= a.dvec) continue;
+                    F2 f[4];
                     unpack8(in[q][v], f);
-                    if (v * G + i < a.dvec) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) rstd[q] += (f[j] - mean[q]) * (f[j] - mean[q]);
-                    }
+                    for (int j = 0; j < 4; ++j) f[j] = add2(f[j], minus);
+                    sum = fma2(f[1], f[1], fma2(f[0], f[0], sum));
+                    sum2 = fma2(f[3], f[3], fma2(f[2], f[2], sum2));
                 }
+                sum = add2(sum, sum2);
+                rstd[q] = unf2(sum).x + unf2(sum).y;
             }
             group_sum<S, R>(rstd, sm, flip);
 #pragma unroll
             for (int q = 0; q < R; ++q) rstd[q] = 1.f / sqrtf(rstd[q] * a.inv_d + a.eps);
         }
+        if (a.stats && i == 0) {
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int64_t t = token[q], r = row_of<S>(st, group * R + q);
-            if (t < 0) continue;
-            if (a.stats && i == 0) a.stats[r] = make_float2(mean[q], rstd[q]);
+            for (int q = 0; q < R; ++q)
+                if (token[q] >= 0) a.stats[row_of<S>(st, group * R + q)] = make_float2(mean[q], rstd[q]);
+        }
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * G + i;
+        for (int v = 0; v < V; ++v) {
+            const int c = v * G + i;
+            F2 wf[4], bf[4];
+            unpack8(w[v], wf);
+            unpack8(b[v], bf);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const int64_t t = token[q], r = row_of<S>(st, group * R + q);
+                if (t < 0) continue;  // the same for the whole group
                 if (a.c.format >= 0) {
                     const uint32_t code = ckpt::scale_code(in[q][v], a.c.format);
                     if (c < a.dvec) ckpt::store8(a.c, r, c, in[q][v], code);
                 }
                 if (c >= a.dvec) continue;
-                float f[8], wf[8], bf[8];
+                F2 f[4];
                 unpack8(in[q][v], f);
-                unpack8(w[v], wf);
-                unpack8(b[v], bf);
+                const F2 minus = two(-mean[q]), rs = two(rstd[q]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean[q]) * rstd[q], wf[j], bf[j]);
+                for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(add2(f[j], minus), rs), wf[j], bf[j]);
                 if (POST) {
                     const uint32_t row = row0 + q * a.slot;
-                    float gf[8], xf[8];
+                    F2 gf[4], xf[4];
                     unpack8(a.streams == 3 ? ld_shared(row + a.in[2].off + 16 * c) : gate[v], gf);
                     unpack8(ld_shared(row + a.in[1].off + 16 * c), xf);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) xf[j] += a.scale * (gf[j] * f[j]);
+                    for (int j = 0; j < 4; ++j) xf[j] = fma2(two(a.scale), mul2(gf[j], f[j]), xf[j]);
                     a.x[t * a.ld_x + c] = pack8(xf);
                 } else {
                     a.y[r * a.ld_y + c] = pack8(f);
@@ -443,13 +462,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     int flip = 0;
     const bool coded = a.c.format >= 0;
     uint4 w[V];
-    float s1[8 * V], s2[S2 ? 8 * V : 1];
+    F2 s1[4 * V], s2[S2 ? 4 * V : 1];
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = ld_or(a.w, v * G + i, v * G + i < a.dvec, kOnes);
 #pragma unroll
-    for (int j = 0; j < 8 * V; ++j) {
-        s1[j] = 0.f;
-        if (S2) s2[j] = 0.f;
+    for (int j = 0; j < 4 * V; ++j) {
+        s1[j] = two(0.f);
+        if (S2) s2[j] = two(0.f);
     }
     // scale bytes of this group's next rows
     uint32_t code[R][V];
@@ -493,68 +512,77 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                 }
                 raw_g[q][v] = ld_shared(row + a.in[1].off + 16 * c);
             }
-        auto vhat = [&](int q, int v, float* f) {
+        auto vhat = [&](int q, int v, F2* f) {
             const float2 m = stats[q];  // (mean, rstd)
             if (coded)
                 ckpt::decode8(make_uint2(raw_v[q][v].x, raw_v[q][v].y), code[q][v], a.c.format, f);
             else
                 unpack8(raw_v[q][v], f);
+            const F2 minus = two(-m.x), rs = two(m.y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = (f[j] - m.x) * m.y;  // no cancellation next to the mean
+            for (int j = 0; j < 4; ++j) f[j] = mul2(add2(f[j], minus), rs);  // no cancellation next to the mean
         };
         // gate of vector v (POST)
-        auto gated = [&](int q, int v, float* gf) {
+        auto gated = [&](int q, int v, F2* gf) {
             const int c = v * G + i;
             unpack8(a.ld_gate ? ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c)
                               : ld_or(a.gate, c, true, kOnes), gf);
         };
-        float p[2 * R];
+        F2 p1[R], p2[R];
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            p[q] = p[R + q] = 0.f;
-            if (token[q] < 0) continue;  // no row: nothing goes into the sums
+        for (int q = 0; q < R; ++q) p1[q] = p2[q] = two(0.f);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * G + i;
-                if (c >= a.dvec) continue;
-                float vv[8], gg[8], wf[8];
+        for (int v = 0; v < V; ++v) {
+            const int c = v * G + i;
+            if (c >= a.dvec) continue;
+            F2 wf[4];
+            unpack8(w[v], wf);
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (token[q] < 0) continue;  // no row: nothing goes into the sums
+                F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 unpack8(raw_g[q][v], gg);
-                unpack8(w[v], wf);
                 if (POST) {
-                    float gf[8];
+                    F2 gf[4];
                     gated(q, v, gf);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) gg[j] *= a.scale;
+                    for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], two(a.scale));
                     if (a.dgate_rows) {
-                        float bf[8];
+                        F2 bf[4];
                         unpack8(ld_or(a.b, c, true, 0u), bf);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) bf[j] = gg[j] * (vv[j] * wf[j] + bf[j]);
+                        for (int j = 0; j < 4; ++j) bf[j] = mul2(gg[j], fma2(vv[j], wf[j], bf[j]));
                         a.dgate_rows[row_of<S>(st, group * R + q) * a.ld_dgate + c] = pack8(bf);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float dn = gg[j] * gf[j];
-                        const float sum = a.ld_gate ? dn : gg[j];
-                        s1[8 * v + j] += sum * vv[j];
-                        if (S2) s2[8 * v + j] += sum;
+                    for (int j = 0; j < 4; ++j) {
+                        const F2 dn = mul2(gg[j], gf[j]);
+                        const F2 sum = a.ld_gate ? dn : gg[j];
+                        s1[4 * v + j] = fma2(sum, vv[j], s1[4 * v + j]);
+                        if (S2) s2[4 * v + j] = add2(s2[4 * v + j], sum);
                         gg[j] = dn;
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        s1[8 * v + j] += gg[j] * vv[j];
-                        if (S2) s2[8 * v + j] += gg[j];
+                    for (int j = 0; j < 4; ++j) {
+                        s1[4 * v + j] = fma2(gg[j], vv[j], s1[4 * v + j]);
+                        if (S2) s2[4 * v + j] = add2(s2[4 * v + j], gg[j]);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    gg[j] *= wf[j];
-                    p[q] += gg[j] * vv[j];
-                    p[R + q] += gg[j];
+                for (int j = 0; j < 4; ++j) {
+                    gg[j] = mul2(gg[j], wf[j]);
+                    p1[q] = fma2(gg[j], vv[j], p1[q]);
+                    p2[q] = add2(p2[q], gg[j]);
                 }
             }
+        }
+        float p[2 * R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            p[q] = unf2(p1[q]).x + unf2(p1[q]).y;
+            p[R + q] = unf2(p2[q]).x + unf2(p2[q]).y;
         }
         if (a.kind != kNoNorm) {
             group_sum<S, 2 * R>(p, sm, flip);
@@ -568,37 +596,39 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             for (int q = 0; q < 2 * R; ++q) p[q] = 0.f;
         }
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int64_t t = token[q], r = row_of<S>(st, group * R + q);
-            if (t < 0) continue;
-            const float rstd = stats[q].y;
+        for (int v = 0; v < V; ++v) {
+            const int c = v * G + i;
+            if (c >= a.dvec) continue;
+            F2 wf[4];
+            unpack8(w[v], wf);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * G + i;
-                if (c >= a.dvec) continue;
+            for (int q = 0; q < R; ++q) {
+                const int64_t t = token[q], r = row_of<S>(st, group * R + q);
+                if (t < 0) continue;
                 // opaque: or the compiler keeps the unpacked values of the first pass instead
                 asm volatile("" : "+r"(raw_v[q][v].x), "+r"(raw_v[q][v].y), "+r"(raw_v[q][v].z),
                              "+r"(raw_v[q][v].w), "+r"(raw_g[q][v].x), "+r"(raw_g[q][v].y),
                              "+r"(raw_g[q][v].z), "+r"(raw_g[q][v].w));
-                float vv[8], gg[8], wf[8];
+                F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 unpack8(raw_g[q][v], gg);
-                unpack8(w[v], wf);
                 if (POST) {
-                    float gf[8];
+                    F2 gf[4];
                     gated(q, v, gf);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) gg[j] = gg[j] * a.scale * gf[j];
+                    for (int j = 0; j < 4; ++j) gg[j] = mul2(mul2(gg[j], two(a.scale)), gf[j]);
                 }
+                const F2 rs = two(stats[q].y), c1 = two(-p[q]), c2 = two(-p[R + q]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) gg[j] = rstd * (gg[j] * wf[j] - vv[j] * p[q] - p[R + q]);
+                for (int j = 0; j < 4; ++j)
+                    gg[j] = mul2(add2(fma2(vv[j], c1, mul2(gg[j], wf[j])), c2), rs);
                 if (POST) {
                     a.y[r * a.ld_y + c] = pack8(gg);
                 } else {
-                    float xf[8];
+                    F2 xf[4];
                     unpack8(ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c), xf);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) gg[j] += xf[j];
+                    for (int j = 0; j < 4; ++j) gg[j] = add2(gg[j], xf[j]);
                     a.x[t * a.ld_x + c] = pack8(gg);
                 }
             }
@@ -613,6 +643,16 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     }
     if (!a.part || blockIdx.x >= K) return;
     // column sums of this CTA: its groups in order, through the ring (every copy was consumed)
+    float f1[8 * V], f2s[S2 ? 8 * V : 1];
+#pragma unroll
+    for (int j = 0; j < 4 * V; ++j) {
+        f1[2 * j] = unf2(s1[j]).x;
+        f1[2 * j + 1] = unf2(s1[j]).y;
+        if (S2) {
+            f2s[2 * j] = unf2(s2[j]).x;
+            f2s[2 * j + 1] = unf2(s2[j]).y;
+        }
+    }
     if constexpr (NG > 1) {
         float* acc = reinterpret_cast<float*>(smem_raw + kRing);
         for (int gi = 0; gi < NG; ++gi) {
@@ -626,23 +666,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                     for (int j = 0; j < 8; ++j) {
                         // column 8 c + j at [j][c]: neighbouring threads in neighbouring words
                         const int at = j * a.dvec + c;
-                        acc[at] = gi ? acc[at] + s1[8 * v + j] : s1[8 * v + j];
-                        if (S2) acc[a.d + at] = gi ? acc[a.d + at] + s2[8 * v + j] : s2[8 * v + j];
+                        f1[8 * v + j] += gi ? acc[at] : 0.f;
+                        acc[at] = f1[8 * v + j];
+                        if (S2) {
+                            f2s[8 * v + j] += gi ? acc[a.d + at] : 0.f;
+                            acc[a.d + at] = f2s[8 * v + j];
+                        }
                     }
                 }
             }
         }
         if (group != NG - 1) return;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * G + i;
-            if (c >= a.dvec) continue;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s1[8 * v + j] = acc[j * a.dvec + c];
-                if (S2) s2[8 * v + j] = acc[a.d + j * a.dvec + c];
-            }
-        }
     }
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
 #pragma unroll
@@ -652,10 +686,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
             *reinterpret_cast<float4*>(part + 8 * c + j) =
-                make_float4(s1[8 * v + j], s1[8 * v + j + 1], s1[8 * v + j + 2], s1[8 * v + j + 3]);
+                make_float4(f1[8 * v + j], f1[8 * v + j + 1], f1[8 * v + j + 2], f1[8 * v + j + 3]);
             if (S2)
-                *reinterpret_cast<float4*>(part + a.d + 8 * c + j) =
-                    make_float4(s2[8 * v + j], s2[8 * v + j + 1], s2[8 * v + j + 2], s2[8 * v + j + 3]);
+                *reinterpret_cast<float4*>(part + a.d + 8 * c + j) = make_float4(
+                    f2s[8 * v + j], f2s[8 * v + j + 1], f2s[8 * v + j + 2], f2s[8 * v + j + 3]);
         }
     }
 }
