@@ -188,9 +188,9 @@ __device__ __forceinline__ void decode4(uint32_t q, F2 s, int format, F2* f) {
     }
 }
 
-// The 8 values (exact in bf16) of two words of codes.
-__device__ __forceinline__ void decode8(uint2 q, uint32_t code, int format, F2* f) {
-    const F2 s = two(code == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(code << 23));
+// The 8 values (exact in bf16) of two words of codes, times `by`.
+__device__ __forceinline__ void decode8(uint2 q, uint32_t code, int format, F2* f, float by = 1.f) {
+    const F2 s = two((code == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(code << 23)) * by);
     decode4(q.x, s, format, f);
     decode4(q.y, s, format, f + 2);
 }

@@ -1195,7 +1195,7 @@ void add_source(lemo::norm::Args& a, const uint16_t* rows, int64_t ld, bool by_t
         add_stream(a, rows, 2 * ld, 2 * (int64_t)a.d, by_token);
 }
 
-template <bool BWD, bool POST, bool S2, typename S>
+template <bool BWD, bool POST, bool FULL, bool CODED, typename S>
 bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* grid_out) {
     namespace nm = lemo::norm;
     const int64_t stage = (int64_t)a.slot * S::kRows;
@@ -1209,12 +1209,12 @@ bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* gr
     if (grid > sms) grid = sms;
     if (grid > nm::kMaxParts) grid = nm::kMaxParts;
     if constexpr (BWD) {
-        if (!allow_smem<nm::backward_kernel<S, POST, S2>>(dev, nm::kMaxSmem)) return false;
-        launch(nm::backward_kernel<S, POST, S2>, (unsigned)grid, S::kThreads, nm::kRing + (size_t)bytes,
+        if (!allow_smem<nm::backward_kernel<S, POST, FULL, CODED>>(dev, nm::kMaxSmem)) return false;
+        launch(nm::backward_kernel<S, POST, FULL, CODED>, (unsigned)grid, S::kThreads, nm::kRing + (size_t)bytes,
                st, a);
     } else {
-        if (!allow_smem<nm::forward_kernel<S, POST>>(dev, nm::kMaxSmem)) return false;
-        launch(nm::forward_kernel<S, POST>, (unsigned)grid, S::kThreads, nm::kRing + (size_t)bytes, st,
+        if (!allow_smem<nm::forward_kernel<S, POST, FULL>>(dev, nm::kMaxSmem)) return false;
+        launch(nm::forward_kernel<S, POST, FULL>, (unsigned)grid, S::kThreads, nm::kRing + (size_t)bytes, st,
                a);
     }
     *grid_out = (int)grid;
@@ -1225,8 +1225,8 @@ bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* gr
 // thread up to 640 threads, then 512 threads with two or four.  Rows per group and
 // stage: as many as keep at least two stages in the ring (a row is up to three
 // streams of 16 dvec bytes).
-template <bool BWD, bool POST, bool S2>
-lemo_status run_norm(lemo::norm::Args& a, cudaStream_t st, int* grid) {
+template <bool BWD, bool POST, bool FULL, bool CODED>
+lemo_status run_norm_as(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     using lemo::norm::Shape;
     int dev = 0;
     const int sms = device_sms(&dev);
@@ -1236,16 +1236,31 @@ lemo_status run_norm(lemo::norm::Args& a, cudaStream_t st, int* grid) {
         a.spin_limit_ns = (uint64_t)g_spin_ns;
     }
     bool ok;
-    if (a.dvec <= 32) ok = launch_norm<BWD, POST, S2, Shape<32, 1, 2>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 64) ok = launch_norm<BWD, POST, S2, Shape<64, 1, 4>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 128) ok = launch_norm<BWD, POST, S2, Shape<128, 1, 4>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 256) ok = launch_norm<BWD, POST, S2, Shape<256, 1, 4>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, S2, Shape<256, 2, 2>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 640) ok = launch_norm<BWD, POST, S2, Shape<640, 1, 2>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, S2, Shape<512, 2, 2>>(a, dev, sms, st, grid);
-    else ok = launch_norm<BWD, POST, S2, Shape<512, 4, 1>>(a, dev, sms, st, grid);
+    if (a.dvec <= 32) ok = launch_norm<BWD, POST, FULL, CODED, Shape<32, 1, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 64) ok = launch_norm<BWD, POST, FULL, CODED, Shape<64, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 128) ok = launch_norm<BWD, POST, FULL, CODED, Shape<128, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 256) ok = launch_norm<BWD, POST, FULL, CODED, Shape<256, 1, 4>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, FULL, CODED, Shape<256, 2, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 640) ok = launch_norm<BWD, POST, FULL, CODED, Shape<640, 1, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, FULL, CODED, Shape<512, 2, 2>>(a, dev, sms, st, grid);
+    else ok = launch_norm<BWD, POST, FULL, CODED, Shape<512, 4, 1>>(a, dev, sms, st, grid);
     const lemo_status e = launch_status();
     return ok ? e : LEMO_ERR_CUDA;
+}
+
+// `full`: see the kernels (forward: a mean or a bias; backward: a mean or the second sums).
+template <bool BWD, bool POST>
+lemo_status run_norm(lemo::norm::Args& a, bool full, cudaStream_t st, int* grid) {
+    if constexpr (!BWD) {
+        return full ? run_norm_as<BWD, POST, true, false>(a, st, grid)
+                    : run_norm_as<BWD, POST, false, false>(a, st, grid);
+    } else if (a.c.format >= 0) {
+        return full ? run_norm_as<BWD, POST, true, true>(a, st, grid)
+                    : run_norm_as<BWD, POST, false, true>(a, st, grid);
+    } else {
+        return full ? run_norm_as<BWD, POST, true, false>(a, st, grid)
+                    : run_norm_as<BWD, POST, false, false>(a, st, grid);
+    }
 }
 
 lemo_status run_column_sums(const lemo::norm::Args& n, int parts, const uint16_t* w,
@@ -1376,7 +1391,8 @@ lemo_status lemo_norm_gather(lemo_norm norm, const uint16_t* x, int64_t ld_x, in
     a.c = view_of(checkpoint);
     add_stream(a, x, 2 * ld_x, 2 * (int64_t)d, true);
     int grid = 0;
-    return run_norm<false, false, false>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
+    return run_norm<false, false>(a, norm == LEMO_NORM_LAYER || bias,
+                                  reinterpret_cast<cudaStream_t>(stream), &grid);
 }
 
 size_t lemo_norm_workspace_size(int32_t d) {
@@ -1417,11 +1433,10 @@ lemo_status lemo_norm_gather_backward(lemo_norm norm, const uint16_t* dy, int64_
     a.part = sums ? static_cast<float*>(ws) : nullptr;
     add_source(a, x, ld_x, true, checkpoint);
     add_stream(a, dy, 2 * ld_dy, 2 * (int64_t)d, false);
-    add_stream(a, dx, 2 * ld_dx, 2 * (int64_t)d, true);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     int grid = 0;
-    const bool second = dbias != nullptr;
-    e = second ? run_norm<true, false, true>(a, st, &grid) : run_norm<true, false, false>(a, st, &grid);
+    const bool second = norm == LEMO_NORM_LAYER || dbias;
+    e = run_norm<true, false>(a, second, st, &grid);
     if (e != LEMO_OK || !sums) return e;
     return run_column_sums(a, grid, nullptr, nullptr, nullptr, dweight, dbias, nullptr, second, st);
 }
@@ -1460,7 +1475,8 @@ lemo_status lemo_norm_scatter(lemo_norm norm, uint16_t* x, int64_t ld_x, int64_t
     add_stream(a, x, 2 * ld_x, 2 * (int64_t)d, true);
     if (ld_gate) add_stream(a, gate, 2 * ld_gate, 2 * (int64_t)d, false);
     int grid = 0;
-    return run_norm<false, true, false>(a, reinterpret_cast<cudaStream_t>(stream), &grid);
+    return run_norm<false, true>(a, norm == LEMO_NORM_LAYER || bias,
+                                 reinterpret_cast<cudaStream_t>(stream), &grid);
 }
 
 lemo_status lemo_norm_scatter_backward(
@@ -1511,8 +1527,8 @@ lemo_status lemo_norm_scatter_backward(
     add_stream(a, dx, 2 * ld_dx, 2 * (int64_t)d, true);
     if (ld_gate) add_stream(a, gate, 2 * ld_gate, 2 * (int64_t)d, false);
     int grid = 0;
-    const bool second = dbias || (dgate && bias);
-    e = second ? run_norm<true, true, true>(a, st, &grid) : run_norm<true, true, false>(a, st, &grid);
+    const bool second = norm == LEMO_NORM_LAYER || dbias || (dgate && bias);
+    e = run_norm<true, true>(a, second, st, &grid);
     if (e != LEMO_OK || !sums) return e;
     return run_column_sums(a, grid, weight, bias, ld_gate == 0 ? gate : nullptr, dweight, dbias,
                            dgate, second, st);

@@ -112,12 +112,12 @@ struct Args {
 struct Smem {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
-    int64_t token[kMaxStages][kMaxRows];  // -1: no row, or refused
+    int32_t token[kMaxStages][kMaxRows];  // -1: no row, or refused
     float2 stats[kMaxStages][kMaxRows];
     float red[2][kMaxWarps][8];           // per consumer warp, two alternating buffers
     int abort_flag;
 };
-constexpr int kRing = 6144;  // offset of the ring
+constexpr int kRing = 5120;  // offset of the ring
 static_assert(sizeof(Smem) <= kRing, "the ring starts behind the barriers");
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Smem* sm, uint64_t limit_ns) {
@@ -248,7 +248,7 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
         if (!(ok = wait_warp(&sm->empty[s], ph ^ 1, sm, a.spin_limit_ns))) break;
         const uint32_t rows = __ballot_sync(0xffffffffu, t >= 0);
         if (lane < NR) {
-            sm->token[s][lane] = t;
+            sm->token[s][lane] = (int32_t)t;
             sm->stats[s][lane] = stat;
         }
         __syncwarp();
@@ -302,9 +302,10 @@ __device__ __forceinline__ void zero_tail(const Args& a, int64_t K, int64_t K_pa
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  Streams: gather x; scatter y, x, (gate rows).
+// Forward.  Streams: gather x; scatter y, x, (gate rows).  FULL: any norm, with
+// or without a bias; otherwise no mean and no bias.
 // ---------------------------------------------------------------------------
-template <typename S, bool POST>
+template <typename S, bool POST, bool FULL>
 __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_constant__ Args a) {
     constexpr int G = S::G, V = S::V, R = S::R;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -323,12 +324,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
     int flip = 0;
-    uint4 w[V], b[V], gate[V];
+    uint4 w[V], b[FULL ? V : 1], gate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = v * G + i;
         w[v] = ld_or(a.w, c, c < a.dvec, kOnes);
-        b[v] = ld_or(a.b, c, c < a.dvec, 0u);
+        if (FULL) b[v] = ld_or(a.b, c, c < a.dvec, 0u);
         if (POST) gate[v] = ld_or(a.ld_gate == 0 ? a.gate : nullptr, c, c < a.dvec, kOnes);
     }
     int s = 0;
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
     for (int64_t st = 0; row_of<S>(st, 0) < K; ++st) {
         if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
         const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
-        const int64_t* token = &sm->token[s][group * R];
+        const int32_t* token = &sm->token[s][group * R];
         uint4 in[R][V];
 #pragma unroll
         for (int q = 0; q < R; ++q)
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
             mean[q] = 0.f;
             rstd[q] = 1.f;
         }
-        if (a.kind == kLayer) {
+        if (FULL && a.kind == kLayer) {
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 F2 sum = two(0.f);
@@ -378,8 +379,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
                     if (v * G + i >= a.dvec) continue;
                     F2 f[4];
                     unpack8(in[q][v], f);
+                    if (FULL) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) f[j] = add2(f[j], minus);
+                        for (int j = 0; j < 4; ++j) f[j] = add2(f[j], minus);
+                    }
                     sum = fma2(f[1], f[1], fma2(f[0], f[0], sum));
                     sum2 = fma2(f[3], f[3], fma2(f[2], f[2], sum2));
                 }
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
             const int c = v * G + i;
             F2 wf[4], bf[4];
             unpack8(w[v], wf);
-            unpack8(b[v], bf);
+            if (FULL) unpack8(b[v], bf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 const int64_t t = token[q], r = row_of<S>(st, group * R + q);
@@ -414,7 +417,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
                 unpack8(in[q][v], f);
                 const F2 minus = two(-mean[q]), rs = two(rstd[q]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(add2(f[j], minus), rs), wf[j], bf[j]);
+                for (int j = 0; j < 4; ++j)
+                    f[j] = FULL ? fma2(mul2(add2(f[j], minus), rs), wf[j], bf[j])
+                                : mul2(mul2(f[j], rs), wf[j]);
                 if (POST) {
                     const uint32_t row = row0 + q * a.slot;
                     F2 gf[4], xf[4];
@@ -438,10 +443,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Streams: the normalised row (bf16 or codes); gather dy, dx;
-// scatter dx, (gate rows).  S2: the sums of dy (dn) are wanted too.
+// Backward.  Streams: the normalised row (bf16, or codes: CODED); gather dy;
+// scatter dx, (gate rows).  FULL: any norm, and the sums of dy (dn) too;
+// otherwise no mean and only the sums with vhat.  Both passes over a row read it
+// from shared memory: holding 2 R V raw vectors per thread over the reduction cost
+// more in registers than the second read.  The row of dx that a gather updates is
+// loaded to registers before the first pass and used after the second.
 // ---------------------------------------------------------------------------
-template <typename S, bool POST, bool S2>
+template <typename S, bool POST, bool FULL, bool CODED>
 __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_constant__ Args a) {
     constexpr int G = S::G, V = S::V, R = S::R, NG = S::kGroups;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -460,27 +469,28 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
     int flip = 0;
-    const bool coded = a.c.format >= 0;
     uint4 w[V];
-    F2 s1[4 * V], s2[S2 ? 4 * V : 1];
+    F2 s1[4 * V], s2[FULL ? 4 * V : 1];
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = ld_or(a.w, v * G + i, v * G + i < a.dvec, kOnes);
 #pragma unroll
     for (int j = 0; j < 4 * V; ++j) {
         s1[j] = two(0.f);
-        if (S2) s2[j] = two(0.f);
+        if (FULL) s2[j] = two(0.f);
     }
     // scale bytes of this group's next rows
-    uint32_t code[R][V];
+    uint32_t code[CODED ? R : 1][V];
     auto load_codes = [&](int64_t st) {
-        if (!coded) return;
+        if constexpr (CODED) {
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int64_t r = row_of<S>(st, group * R + q);
+            for (int q = 0; q < R; ++q) {
+                const int64_t r = row_of<S>(st, group * R + q);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * G + i;
-                code[q][v] = r < K && c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
+                for (int v = 0; v < V; ++v) {
+                    const int c = v * G + i;
+                    code[q][v] =
+                        r < K && c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
+                }
             }
         }
     };
@@ -490,43 +500,48 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     for (int64_t st = 0; row_of<S>(st, 0) < K; ++st) {
         if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
         const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
-        const int64_t* token = &sm->token[s][group * R];
-        const float2* stats = &sm->stats[s][group * R];
-        // The rows' raw vectors stay in registers over the reduction, not what they unpack to
-        // (a third of the registers); both passes unpack them.
-        uint4 raw_v[R][V], raw_g[R][V];
+        const int32_t* token = &sm->token[s][group * R];
+        const float2* stats = &sm->stats[s][group * R];  // (mean, rstd)
+        uint4 xin[POST ? 1 : R][V];
+        if constexpr (!POST) {
 #pragma unroll
-        for (int q = 0; q < R; ++q)
+            for (int q = 0; q < R; ++q)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = v * G + i;
-                const uint32_t row = row0 + q * a.slot;
-                raw_v[q][v] = raw_g[q][v] = make_uint4(0u, 0u, 0u, 0u);
-                if (token[q] < 0 || c >= a.dvec) continue;
-                if (coded) {
-                    const uint2 k = ld_shared8(row + 8 * c);
-                    raw_v[q][v].x = k.x;
-                    raw_v[q][v].y = k.y;
-                } else {
-                    raw_v[q][v] = ld_shared(row + 16 * c);
+                for (int v = 0; v < V; ++v) {
+                    const int c = v * G + i;
+                    if (token[q] >= 0 && c < a.dvec) xin[q][v] = a.x[token[q] * a.ld_x + c];
                 }
-                raw_g[q][v] = ld_shared(row + a.in[1].off + 16 * c);
-            }
+        }
         auto vhat = [&](int q, int v, F2* f) {
-            const float2 m = stats[q];  // (mean, rstd)
-            if (coded)
-                ckpt::decode8(make_uint2(raw_v[q][v].x, raw_v[q][v].y), code[q][v], a.c.format, f);
-            else
-                unpack8(raw_v[q][v], f);
-            const F2 minus = two(-m.x), rs = two(m.y);
+            const int c = v * G + i;
+            const uint32_t row = row0 + q * a.slot;
+            const float2 m = stats[q];
+            if constexpr (CODED) {
+                // without a mean, rstd goes into the power-of-two scale: the same values
+                ckpt::decode8(ld_shared8(row + 8 * c), code[q][v], a.c.format, f, FULL ? 1.f : m.y);
+            } else {
+                unpack8(ld_shared(row + 16 * c), f);
+            }
+            if (FULL) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = mul2(add2(f[j], minus), rs);  // no cancellation next to the mean
+                for (int j = 0; j < 4; ++j) f[j] = mul2(add2(f[j], two(-m.x)), two(m.y));
+            } else if (!CODED) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], two(m.y));
+            }
         };
-        // gate of vector v (POST)
-        auto gated = [&](int q, int v, F2* gf) {
+        // gradient of the row's output (POST: of n, with the scale, before the gate)
+        auto grad = [&](int q, int v, F2* f) {
+            unpack8(ld_shared(row0 + q * a.slot + a.in[1].off + 16 * (v * G + i)), f);
+            if (POST) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], two(a.scale));
+            }
+        };
+        auto gated = [&](int q, int v, F2* f) {
             const int c = v * G + i;
             unpack8(a.ld_gate ? ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c)
-                              : ld_or(a.gate, c, true, kOnes), gf);
+                              : ld_or(a.gate, c, true, kOnes), f);
         };
         F2 p1[R], p2[R];
 #pragma unroll
@@ -542,12 +557,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                 if (token[q] < 0) continue;  // no row: nothing goes into the sums
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
-                unpack8(raw_g[q][v], gg);
+                grad(q, v, gg);
                 if (POST) {
                     F2 gf[4];
                     gated(q, v, gf);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], two(a.scale));
                     if (a.dgate_rows) {
                         F2 bf[4];
                         unpack8(ld_or(a.b, c, true, 0u), bf);
@@ -560,41 +573,35 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                         const F2 dn = mul2(gg[j], gf[j]);
                         const F2 sum = a.ld_gate ? dn : gg[j];
                         s1[4 * v + j] = fma2(sum, vv[j], s1[4 * v + j]);
-                        if (S2) s2[4 * v + j] = add2(s2[4 * v + j], sum);
+                        if (FULL) s2[4 * v + j] = add2(s2[4 * v + j], sum);
                         gg[j] = dn;
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         s1[4 * v + j] = fma2(gg[j], vv[j], s1[4 * v + j]);
-                        if (S2) s2[4 * v + j] = add2(s2[4 * v + j], gg[j]);
+                        if (FULL) s2[4 * v + j] = add2(s2[4 * v + j], gg[j]);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     gg[j] = mul2(gg[j], wf[j]);
                     p1[q] = fma2(gg[j], vv[j], p1[q]);
-                    p2[q] = add2(p2[q], gg[j]);
+                    if (FULL) p2[q] = add2(p2[q], gg[j]);
                 }
             }
         }
-        float p[2 * R];
+        constexpr int P = FULL ? 2 * R : R;  // mean(g vhat), and mean(g) behind it
+        float p[P];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             p[q] = unf2(p1[q]).x + unf2(p1[q]).y;
-            p[R + q] = unf2(p2[q]).x + unf2(p2[q]).y;
+            if (FULL) p[P - R + q] = unf2(p2[q]).x + unf2(p2[q]).y;
         }
-        if (a.kind != kNoNorm) {
-            group_sum<S, 2 * R>(p, sm, flip);
+        if (a.kind != kNoNorm) group_sum<S, P>(p, sm, flip);
 #pragma unroll
-            for (int q = 0; q < R; ++q) {
-                p[q] *= a.inv_d;
-                p[R + q] = a.kind == kLayer ? p[R + q] * a.inv_d : 0.f;
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2 * R; ++q) p[q] = 0.f;
-        }
+        for (int q = 0; q < P; ++q)
+            p[q] = a.kind == kNoNorm || (q >= R && a.kind != kLayer) ? 0.f : -p[q] * a.inv_d;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * G + i;
@@ -603,32 +610,32 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             unpack8(w[v], wf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                const int64_t t = token[q], r = row_of<S>(st, group * R + q);
+                const int64_t t = token[q];
                 if (t < 0) continue;
-                // opaque: or the compiler keeps the unpacked values of the first pass instead
-                asm volatile("" : "+r"(raw_v[q][v].x), "+r"(raw_v[q][v].y), "+r"(raw_v[q][v].z),
-                             "+r"(raw_v[q][v].w), "+r"(raw_g[q][v].x), "+r"(raw_g[q][v].y),
-                             "+r"(raw_g[q][v].z), "+r"(raw_g[q][v].w));
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
-                unpack8(raw_g[q][v], gg);
+                grad(q, v, gg);
                 if (POST) {
                     F2 gf[4];
                     gated(q, v, gf);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) gg[j] = mul2(mul2(gg[j], two(a.scale)), gf[j]);
+                    for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], gf[j]);
                 }
-                const F2 rs = two(stats[q].y), c1 = two(-p[q]), c2 = two(-p[R + q]);
+                const F2 rs = two(stats[q].y), c1 = two(p[q]), c2 = two(FULL ? p[P - R + q] : 0.f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    gg[j] = mul2(add2(fma2(vv[j], c1, mul2(gg[j], wf[j])), c2), rs);
-                if (POST) {
-                    a.y[r * a.ld_y + c] = pack8(gg);
+                for (int j = 0; j < 4; ++j) {
+                    gg[j] = fma2(vv[j], c1, mul2(gg[j], wf[j]));
+                    if (FULL) gg[j] = add2(gg[j], c2);
+                }
+                if constexpr (POST) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], rs);
+                    a.y[row_of<S>(st, group * R + q) * a.ld_y + c] = pack8(gg);
                 } else {
                     F2 xf[4];
-                    unpack8(ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c), xf);
+                    unpack8(xin[q][v], xf);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) gg[j] = add2(gg[j], xf[j]);
+                    for (int j = 0; j < 4; ++j) gg[j] = fma2(gg[j], rs, xf[j]);
                     a.x[t * a.ld_x + c] = pack8(gg);
                 }
             }
@@ -643,12 +650,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     }
     if (!a.part || blockIdx.x >= K) return;
     // column sums of this CTA: its groups in order, through the ring (every copy was consumed)
-    float f1[8 * V], f2s[S2 ? 8 * V : 1];
+    float f1[8 * V], f2s[FULL ? 8 * V : 1];
 #pragma unroll
     for (int j = 0; j < 4 * V; ++j) {
         f1[2 * j] = unf2(s1[j]).x;
         f1[2 * j + 1] = unf2(s1[j]).y;
-        if (S2) {
+        if (FULL) {
             f2s[2 * j] = unf2(s2[j]).x;
             f2s[2 * j + 1] = unf2(s2[j]).y;
         }
@@ -668,7 +675,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                         const int at = j * a.dvec + c;
                         f1[8 * v + j] += gi ? acc[at] : 0.f;
                         acc[at] = f1[8 * v + j];
-                        if (S2) {
+                        if (FULL) {
                             f2s[8 * v + j] += gi ? acc[a.d + at] : 0.f;
                             acc[a.d + at] = f2s[8 * v + j];
                         }
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
         for (int j = 0; j < 8; j += 4) {
             *reinterpret_cast<float4*>(part + 8 * c + j) =
                 make_float4(f1[8 * v + j], f1[8 * v + j + 1], f1[8 * v + j + 2], f1[8 * v + j + 3]);
-            if (S2)
+            if (FULL)
                 *reinterpret_cast<float4*>(part + a.d + 8 * c + j) = make_float4(
                     f2s[8 * v + j], f2s[8 * v + j + 1], f2s[8 * v + j + 2], f2s[8 * v + j + 3]);
         }
