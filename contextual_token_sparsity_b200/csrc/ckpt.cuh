@@ -132,40 +132,32 @@ __device__ __forceinline__ uint32_t low_bytes(F2 a, F2 b) {
 // magnitude next to 2^128 could round up to 2^128 (247, 249), and 255.
 constexpr uint32_t kRareCode = 247;
 
-__device__ __noinline__ uint2 encode8_rare(uint4 v, uint32_t code, int format) {
-    if (code == 255u) {
-        const uint32_t q = format == kE4M3 ? 0x7f7f7f7fu : 0u;
-        return make_uint2(q, q);
-    }
-    const float inv = __uint_as_float((254u - code) << 23);  // 2^-k
-    const float most = code != (format == kE4M3 ? 247u : 249u) ? 448.f : format == kE4M3 ? 240.f : 63.f;
-    F2 f[4];
-    unpack8(v, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 t = unf2(f[i]);
-        t.x = fminf(fmaxf(t.x * inv, -most), most);
-        t.y = fminf(fmaxf(t.y * inv, -most), most);
-        f[i] = format == kE4M3 ? f2(t.x, t.y) : f2(t.x + kMagic, t.y + kMagic);
-    }
-    return format == kE4M3 ? make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]))
-                           : make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
-}
-
 // Codes of 8 values under the group's scale byte.
 __device__ __forceinline__ uint2 encode8(uint4 v, uint32_t code, int format) {
-    if (code >= kRareCode) return encode8_rare(v, code, format);
     const F2 inv = two(__uint_as_float((254u - code) << 23));  // 2^-k
     F2 f[4];
     unpack8(v, f);
+    if (code >= kRareCode) {
+        const float most = (code != (format == kE4M3 ? 247u : 249u) ? 448.f : format == kE4M3 ? 240.f : 63.f) *
+                           __uint_as_float(code << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = unf2(f[i]);
+            f[i] = f2(fminf(fmaxf(t.x, -most), most), fminf(fmaxf(t.y, -most), most));
+        }
+    }
+    uint2 q;
     if (format == kE4M3) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], inv);
-        return make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]));
-    }
+        q = make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = fma2(f[i], inv, two(kMagic));
-    return make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
+        for (int i = 0; i < 4; ++i) f[i] = fma2(f[i], inv, two(kMagic));
+        q = make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
+    }
+    const uint32_t none = format == kE4M3 ? 0x7f7f7f7fu : 0u;  // a group that is not finite
+    return make_uint2(code == 255u ? none : q.x, code == 255u ? none : q.y);
 }
 
 __device__ __forceinline__ void decode4(uint32_t q, F2 s, int format, F2* f) {
@@ -195,9 +187,11 @@ __device__ __forceinline__ void decode8(uint2 q, uint32_t code, int format, F2* 
     decode4(q.y, s, format, f + 2);
 }
 
-__device__ __forceinline__ void store8(const View& c, int64_t r, int vec, uint4 v, uint32_t code) {
-    *reinterpret_cast<uint2*>(c.data + r * c.ld + 8 * (int64_t)vec) = encode8(v, code, c.format);
-    if ((vec & 3) == 0) c.scales[r * c.ld_scales + (vec >> 2)] = (uint8_t)code;
+// Vector `vec` of a row: `data` and `scales` point at the row's first code and scale.
+__device__ __forceinline__ void store8(uint8_t* data, uint8_t* scales, int format, int vec, uint4 v,
+                                       uint32_t code) {
+    *reinterpret_cast<uint2*>(data + 8 * vec) = encode8(v, code, format);
+    if ((vec & 3) == 0) scales[vec >> 2] = (uint8_t)code;
 }
 
 // Rows that exist on the device: kept_total clamped to the buffers' rows.
@@ -249,6 +243,8 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const RowsArgs a) {
             continue;
         }
         const uint4* src = a.x + t * a.ld;
+        uint8_t* data = a.c.data + r * a.c.ld;
+        uint8_t* scales = a.c.scales + r * a.c.ld_scales;
         for (int c0 = 0; c0 < a.dvec; c0 += 32 * kUnroll) {
             uint4 v[kUnroll];
 #pragma unroll
@@ -261,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const RowsArgs a) {
                 const int c = c0 + 32 * u + lane;
                 if (c0 + 32 * u >= a.dvec) break;  // warp-uniform
                 const uint32_t code = scale_code(v[u], a.c.format);
-                if (c < a.dvec) store8(a.c, r, c, v[u], code);
+                if (c < a.dvec) store8(data, scales, a.c.format, c, v[u], code);
             }
         }
     }
@@ -370,11 +366,15 @@ __global__ void __launch_bounds__(kThreads, 4) gated_kernel(const GatedArgs p) {
             if (r[k] < K) {
                 if (p.cg.format >= 0) {
                     const uint32_t code = scale_code(g[k], p.cg.format);
-                    if (in) store8(p.cg, r[k], c[k], g[k], code);
+                    if (in)
+                        store8(p.cg.data + r[k] * p.cg.ld, p.cg.scales + r[k] * p.cg.ld_scales, p.cg.format,
+                               c[k], g[k], code);
                 }
                 if (p.cu.format >= 0) {
                     const uint32_t code = scale_code(u[k], p.cu.format);
-                    if (in) store8(p.cu, r[k], c[k], u[k], code);
+                    if (in)
+                        store8(p.cu.data + r[k] * p.cu.ld, p.cu.scales + r[k] * p.cu.ld_scales, p.cu.format,
+                               c[k], u[k], code);
                 }
             }
             F2 gf[4], uf[4];  // a row of the tail: zeros, SiLU(0) 0 = 0

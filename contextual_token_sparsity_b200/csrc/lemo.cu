@@ -8,6 +8,7 @@
 
 #include <climits>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "lemo.h"
@@ -1240,7 +1241,9 @@ lemo_status run_norm_as(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     else if (a.dvec <= 64) ok = launch_norm<BWD, POST, FULL, CODED, Shape<64, 1, 4>>(a, dev, sms, st, grid);
     else if (a.dvec <= 128) ok = launch_norm<BWD, POST, FULL, CODED, Shape<128, 1, 4>>(a, dev, sms, st, grid);
     else if (a.dvec <= 256) ok = launch_norm<BWD, POST, FULL, CODED, Shape<256, 1, 4>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 512) ok = launch_norm<BWD, POST, FULL, CODED, Shape<256, 2, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 512)
+        ok = launch_norm<BWD, POST, FULL, CODED, std::conditional_t<BWD && FULL, Shape<512, 1, 4>, Shape<256, 2, 2>>>(
+            a, dev, sms, st, grid);
     else if (a.dvec <= 640) ok = launch_norm<BWD, POST, FULL, CODED, Shape<640, 1, 2>>(a, dev, sms, st, grid);
     else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, FULL, CODED, Shape<512, 2, 2>>(a, dev, sms, st, grid);
     else ok = launch_norm<BWD, POST, FULL, CODED, Shape<512, 4, 1>>(a, dev, sms, st, grid);

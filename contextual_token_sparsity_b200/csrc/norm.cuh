@@ -391,12 +391,21 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
             }
             group_sum<S, R>(rstd, sm, flip);
 #pragma unroll
-            for (int q = 0; q < R; ++q) rstd[q] = 1.f / sqrtf(rstd[q] * a.inv_d + a.eps);
+            for (int q = 0; q < R; ++q) rstd[q] = rsqrtf(rstd[q] * a.inv_d + a.eps);
         }
         if (a.stats && i == 0) {
 #pragma unroll
             for (int q = 0; q < R; ++q)
                 if (token[q] >= 0) a.stats[row_of<S>(st, group * R + q)] = make_float2(mean[q], rstd[q]);
+        }
+        uint4* out[R];
+        uint8_t *data[R], *scales[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = row_of<S>(st, group * R + q);
+            out[q] = POST ? a.x + (int64_t)token[q] * a.ld_x : a.y + r * a.ld_y;
+            data[q] = a.c.data + r * a.c.ld;
+            scales[q] = a.c.scales + r * a.c.ld_scales;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -406,11 +415,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
             if (FULL) unpack8(b[v], bf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                const int64_t t = token[q], r = row_of<S>(st, group * R + q);
-                if (t < 0) continue;  // the same for the whole group
+                if (token[q] < 0) continue;  // the same for the whole group
                 if (a.c.format >= 0) {
                     const uint32_t code = ckpt::scale_code(in[q][v], a.c.format);
-                    if (c < a.dvec) ckpt::store8(a.c, r, c, in[q][v], code);
+                    if (c < a.dvec) ckpt::store8(data[q], scales[q], a.c.format, c, in[q][v], code);
                 }
                 if (c >= a.dvec) continue;
                 F2 f[4];
@@ -427,9 +435,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
                     unpack8(ld_shared(row + a.in[1].off + 16 * c), xf);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) xf[j] = fma2(two(a.scale), mul2(gf[j], f[j]), xf[j]);
-                    a.x[t * a.ld_x + c] = pack8(xf);
+                    out[q][c] = pack8(xf);
                 } else {
-                    a.y[r * a.ld_y + c] = pack8(f);
+                    out[q][c] = pack8(f);
                 }
             }
         }
@@ -502,6 +510,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
         const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
         const int32_t* token = &sm->token[s][group * R];
         const float2* stats = &sm->stats[s][group * R];  // (mean, rstd)
+        uint4* out[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            out[q] = POST ? a.y + row_of<S>(st, group * R + q) * a.ld_y : a.x + (int64_t)token[q] * a.ld_x;
         uint4 xin[POST ? 1 : R][V];
         if constexpr (!POST) {
 #pragma unroll
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int c = v * G + i;
-                    if (token[q] >= 0 && c < a.dvec) xin[q][v] = a.x[token[q] * a.ld_x + c];
+                    if (token[q] >= 0 && c < a.dvec) xin[q][v] = out[q][c];
                 }
         }
         auto vhat = [&](int q, int v, F2* f) {
@@ -610,8 +622,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             unpack8(w[v], wf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                const int64_t t = token[q];
-                if (t < 0) continue;
+                if (token[q] < 0) continue;
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 grad(q, v, gg);
@@ -630,13 +641,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                 if constexpr (POST) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], rs);
-                    a.y[row_of<S>(st, group * R + q) * a.ld_y + c] = pack8(gg);
+                    out[q][c] = pack8(gg);
                 } else {
                     F2 xf[4];
                     unpack8(xin[q][v], xf);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) gg[j] = fma2(gg[j], rs, xf[j]);
-                    a.x[t * a.ld_x + c] = pack8(gg);
+                    out[q][c] = pack8(gg);
                 }
             }
         }

@@ -319,30 +319,36 @@ class _Fit:
         err.args = (f"{self.where}: {name} {why}",)
         raise err
 
-    def mat(self, t, name, dtype, cols, rows=0):
-        if t is None:
-            self.bad(name, "is missing")
-        if t.dtype is not dtype or t.dim() != 2:
-            self.bad(name, f"is not a 2-D {dtype} tensor")
-        if t.get_device() != self.dev:
-            self.bad(name, "is not on the current CUDA device")
-        n, width = t.shape
-        if n < rows or width < cols:
-            self.bad(name, f"has shape {(n, width)}, at least {(rows, cols)} is needed")
-        if width > 1 and t.stride(1) != 1:
-            self.bad(name, "does not have contiguous rows")
-        return t.data_ptr()
+    def mat(self, t, name, dtype, cols, rows=0, unit=8):
+        """(pointer, row stride) of a 2-D tensor with contiguous rows; a single
+        row's own stride says nothing, so its width rounded up to `unit` stands in."""
+        if t is not None:
+            shape = t.shape
+            if len(shape) == 2 and t.dtype is dtype and t.get_device() == self.dev:
+                n, width = shape
+                ld, step = t.stride()
+                if n >= rows and width >= cols and (step == 1 or width == 1):
+                    return t.data_ptr(), ld if n > 1 else -(-width // unit) * unit
+        self.explain(t, name, dtype, (rows, cols))
 
     def vec(self, t, name, dtype, n):
         if t is None:
             return None
-        if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n:
-            self.bad(name, f"is not a 1-D {dtype} tensor of at least {n} values")
+        if (t.dtype is dtype and t.dim() == 1 and t.numel() >= n and t.is_contiguous()
+                and t.get_device() == self.dev):
+            return t.data_ptr()
+        self.explain(t, name, dtype, (n,))
+
+    def explain(self, t, name, dtype, need):
+        if t is None:
+            self.bad(name, "is missing")
+        if t.dtype is not dtype or t.dim() != len(need):
+            self.bad(name, f"is not a {len(need)}-D {dtype} tensor")
         if t.get_device() != self.dev:
             self.bad(name, "is not on the current CUDA device")
-        if n != 1 and t.stride(0) != 1 and t.shape[0] > 1:
-            self.bad(name, "is not contiguous")
-        return t.data_ptr()
+        if any(have < want for have, want in zip(t.shape, need)):
+            self.bad(name, f"has shape {tuple(t.shape)}, at least {need} is needed")
+        self.bad(name, "does not have contiguous rows")
 
     def total(self, kept_total):
         if kept_total is None:
@@ -373,25 +379,17 @@ def _device() -> int:
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
-def _ld(t, unit=8):
-    """Row stride of a 2-D tensor (a single row's own stride says nothing)."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // unit) * unit
-
-
 class Checkpoint:
     """Rows in 8 bits: ``data`` uint8 [rows, >= d] (row stride a multiple of 16
     bytes), ``scales`` uint8 [rows, >= ceil(d / 32)] (a multiple of 4)."""
 
     def __init__(self, data, scales, format: int, d: int):
         fit = _Fit("make_checkpoint")
-        fit.mat(data, "data", _UINT8, d)
-        fit.mat(scales, "scales", _UINT8, -(-d // 32), data.shape[0])
+        dp, ld_data = fit.mat(data, "data", _UINT8, d, 0, 16)
+        sp, ld_scales = fit.mat(scales, "scales", _UINT8, -(-d // 32), data.shape[0], 4)
         self.data, self.scales, self.d, self.rows = data, scales, int(d), data.shape[0]
         self.device = data.get_device()
-        self.struct = lemo_checkpoint(int(format), int(d), data.data_ptr(), _ld(data, 16),
-                                      scales.data_ptr(), _ld(scales, 4), data.shape[0])
+        self.struct = lemo_checkpoint(int(format), int(d), dp, ld_data, sp, ld_scales, self.rows)
         self.ref = ctypes.addressof(self.struct)
 
 
@@ -400,26 +398,11 @@ def make_checkpoint(data, scales, format: int, d: int) -> Checkpoint:
     return Checkpoint(data, scales, format, d)
 
 
-def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y, stats=None,
-                     checkpoint=None, stream=None, d=None):
-    """x bf16 [x_rows, >= d], y bf16 [rows, >= d], weight / bias bf16 [d] or
-    None, stats fp32 [rows, 2] contiguous, kept_idx int32 (at least K) or None."""
-    fit = _Fit("lemo_norm_gather")
-    d = x.shape[1] if d is None else d
-    xp, yp, rows = fit.mat(x, "x", _BF16, d), fit.mat(y, "y", _BF16, d), y.shape[0]
-    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
-    _check(load().lemo_norm_gather(
-        int(norm), xp, _ld(x), x.shape[0], int(d), fit.vec(weight, "weight", _BF16, d),
-        fit.vec(bias, "bias", _BF16, d), float(eps), ip, kp, int(pad_to), yp, _ld(y), rows,
-        _stats(fit, stats, rows), fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
-        "lemo_norm_gather")
-
-
 def _stats(fit, stats, rows):
     if stats is None:
         return None
-    p = fit.mat(stats, "stats", _FP32, 2, rows)
-    if stats.shape[1] != 2 or (rows > 1 and stats.stride(0) != 2):
+    p, ld = fit.mat(stats, "stats", _FP32, 2, rows, 2)
+    if ld != 2:
         fit.bad("stats", "is not a contiguous [rows, 2] tensor")
     return p
 
@@ -434,6 +417,32 @@ def _workspace(fit, ws, needed):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _gate(fit, gate, d, rows):
+    if gate is None:
+        return None, 0
+    if gate.dim() == 1:
+        return fit.vec(gate, "gate", _BF16, d), 0
+    return fit.mat(gate, "gate", _BF16, d, rows)
+
+
+def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y, stats=None,
+                     checkpoint=None, stream=None, d=None):
+    """x bf16 [x_rows, >= d], y bf16 [rows, >= d], weight / bias bf16 [d] or
+    None, stats fp32 [rows, 2] contiguous, kept_idx int32 (at least K) or None."""
+    fit = _Fit("lemo_norm_gather")
+    x_rows, width = x.shape
+    d = width if d is None else int(d)
+    rows = y.shape[0]
+    xp, ld_x = fit.mat(x, "x", _BF16, d)
+    yp, ld_y = fit.mat(y, "y", _BF16, d)
+    _check(load().lemo_norm_gather(
+        norm, xp, ld_x, x_rows, d, fit.vec(weight, "weight", _BF16, d),
+        fit.vec(bias, "bias", _BF16, d), eps, fit.vec(kept_idx, "kept_idx", _INT32, 0),
+        fit.total(kept_total), pad_to, yp, ld_y, rows, _stats(fit, stats, rows),
+        fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
+        "lemo_norm_gather")
+
+
 def lemo_norm_workspace_size(d: int) -> int:
     return int(load().lemo_norm_workspace_size(int(d)))
 
@@ -444,26 +453,19 @@ def lemo_norm_gather_backward(norm, dy, weight, stats, kept_idx, kept_total, dx,
     one of x (the forward call's input) and checkpoint; dweight / dbias fp32
     [d] optional (accumulated); ws may be None without them."""
     fit = _Fit("lemo_norm_gather_backward")
-    d = dy.shape[1] if d is None else d
-    rows = dy.shape[0]
-    dyp, dxp = fit.mat(dy, "dy", _BF16, d), fit.mat(dx, "dx", _BF16, d)
-    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
+    rows, width = dy.shape
+    d = width if d is None else int(d)
+    dyp, ld_dy = fit.mat(dy, "dy", _BF16, d)
+    dxp, ld_dx = fit.mat(dx, "dx", _BF16, d)
+    xp, ld_x = (None, 0) if x is None else fit.mat(x, "x", _BF16, d)
     wsp, ws_bytes = _workspace(fit, ws, dweight is not None or dbias is not None)
     _check(load().lemo_norm_gather_backward(
-        int(norm), dyp, _ld(dy), rows, int(d), fit.vec(weight, "weight", _BF16, d),
-        _stats(fit, stats, rows), ip, kp, None if x is None else fit.mat(x, "x", _BF16, d),
-        _ld(x), 0 if x is None else x.shape[0], fit.ckpt(checkpoint, "checkpoint", d, rows),
-        dxp, _ld(dx), dx.shape[0], fit.vec(dweight, "dweight", _FP32, d),
-        fit.vec(dbias, "dbias", _FP32, d), wsp, ws_bytes, _stream(stream)),
+        norm, dyp, ld_dy, rows, d, fit.vec(weight, "weight", _BF16, d), _stats(fit, stats, rows),
+        fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total), xp, ld_x,
+        0 if x is None else x.shape[0], fit.ckpt(checkpoint, "checkpoint", d, rows), dxp, ld_dx,
+        dx.shape[0], fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), wsp,
+        ws_bytes, _stream(stream)),
         "lemo_norm_gather_backward")
-
-
-def _gate(fit, gate, d, rows):
-    if gate is None:
-        return None, 0
-    if gate.dim() == 1:
-        return fit.vec(gate, "gate", _BF16, d), 0
-    return fit.mat(gate, "gate", _BF16, d, rows), _ld(gate)
 
 
 def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept_total,
@@ -471,15 +473,16 @@ def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept
     """x bf16 [tokens, >= d] (updated in place), y bf16 [rows, >= d]; gate None,
     bf16 [d] (all tokens) or bf16 [rows, >= d] (per kept row)."""
     fit = _Fit("lemo_norm_scatter")
-    d = x.shape[1] if d is None else d
+    x_rows, width = x.shape
+    d = width if d is None else int(d)
     rows = y.shape[0]
-    xp, yp = fit.mat(x, "x", _BF16, d), fit.mat(y, "y", _BF16, d)
-    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
+    xp, ld_x = fit.mat(x, "x", _BF16, d)
+    yp, ld_y = fit.mat(y, "y", _BF16, d)
     gp, ld_gate = _gate(fit, gate, d, rows)
     _check(load().lemo_norm_scatter(
-        int(norm), xp, _ld(x), x.shape[0], int(d), yp, _ld(y), rows,
-        fit.vec(weight, "weight", _BF16, d), fit.vec(bias, "bias", _BF16, d), float(eps), gp,
-        ld_gate, float(scale), ip, kp, _stats(fit, stats, rows),
+        norm, xp, ld_x, x_rows, d, yp, ld_y, rows, fit.vec(weight, "weight", _BF16, d),
+        fit.vec(bias, "bias", _BF16, d), eps, gp, ld_gate, scale,
+        fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total), _stats(fit, stats, rows),
         fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
         "lemo_norm_scatter")
 
@@ -491,22 +494,26 @@ def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_
     of y and checkpoint; dgate fp32 [d] (accumulated) for a gate of one row,
     bf16 [rows, >= d] (written) for a gate row per kept row."""
     fit = _Fit("lemo_norm_scatter_backward")
-    d = dx.shape[1] if d is None else d
+    dx_rows, width = dx.shape
+    d = width if d is None else int(d)
     rows = dy.shape[0]
-    dxp, dyp = fit.mat(dx, "dx", _BF16, d), fit.mat(dy, "dy", _BF16, d)
-    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
+    dxp, ld_dx = fit.mat(dx, "dx", _BF16, d)
+    dyp, ld_dy = fit.mat(dy, "dy", _BF16, d)
+    yp, ld_y = (None, 0) if y is None else fit.mat(y, "y", _BF16, d, rows)
     gp, ld_gate = _gate(fit, gate, d, rows)
-    per_row = dgate is not None and dgate.dim() == 2
-    dg = None if per_row else fit.vec(dgate, "dgate", _FP32, d)
-    dgr = fit.mat(dgate, "dgate", _BF16, d, rows) if per_row else None
+    dg, dgr, ld_dgr = None, None, 0
+    if dgate is not None and dgate.dim() == 2:
+        dgr, ld_dgr = fit.mat(dgate, "dgate", _BF16, d, rows)
+    else:
+        dg = fit.vec(dgate, "dgate", _FP32, d)
     wsp, ws_bytes = _workspace(fit, ws, dweight is not None or dbias is not None or dg is not None)
     _check(load().lemo_norm_scatter_backward(
-        int(norm), dxp, _ld(dx), dx.shape[0], int(d), fit.vec(weight, "weight", _BF16, d),
-        fit.vec(bias, "bias", _BF16, d), _stats(fit, stats, rows), gp, ld_gate, float(scale), ip,
-        kp, None if y is None else fit.mat(y, "y", _BF16, d, rows), _ld(y),
-        fit.ckpt(checkpoint, "checkpoint", d, rows), int(pad_to), dyp, _ld(dy), rows,
-        fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), dg, dgr,
-        _ld(dgate) if per_row else 0, wsp, ws_bytes, _stream(stream)),
+        norm, dxp, ld_dx, dx_rows, d, fit.vec(weight, "weight", _BF16, d),
+        fit.vec(bias, "bias", _BF16, d), _stats(fit, stats, rows), gp, ld_gate, scale,
+        fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total), yp, ld_y,
+        fit.ckpt(checkpoint, "checkpoint", d, rows), pad_to, dyp, ld_dy, rows,
+        fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), dg, dgr, ld_dgr,
+        wsp, ws_bytes, _stream(stream)),
         "lemo_norm_scatter_backward")
 
 
@@ -514,33 +521,35 @@ def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
     """x bf16 [tokens, >= checkpoint.d]; kept_idx int32 or None (row r is token r)."""
     fit = _Fit("lemo_checkpoint_save")
     d = checkpoint.d
-    ip, kp = fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total)
-    _check(load().lemo_checkpoint_save(fit.mat(x, "x", _BF16, d), _ld(x), x.shape[0], ip, kp,
-                                       fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream)),
-           "lemo_checkpoint_save")
+    xp, ld_x = fit.mat(x, "x", _BF16, d)
+    _check(load().lemo_checkpoint_save(
+        xp, ld_x, x.shape[0], fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total),
+        fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream)),
+        "lemo_checkpoint_save")
 
 
 def lemo_checkpoint_restore(checkpoint, kept_total, pad_to, y, stream=None):
     """y bf16 [rows, >= checkpoint.d], rows <= checkpoint.rows."""
     fit = _Fit("lemo_checkpoint_restore")
-    d = checkpoint.d
-    kp = fit.total(kept_total)
-    yp = fit.mat(y, "y", _BF16, d)
-    _check(load().lemo_checkpoint_restore(fit.ckpt(checkpoint, "checkpoint", d, y.shape[0]), kp,
-                                          int(pad_to), yp, _ld(y), y.shape[0], _stream(stream)),
-           "lemo_checkpoint_restore")
+    d, rows = checkpoint.d, y.shape[0]
+    yp, ld_y = fit.mat(y, "y", _BF16, d)
+    _check(load().lemo_checkpoint_restore(
+        fit.ckpt(checkpoint, "checkpoint", d, rows), fit.total(kept_total), pad_to, yp, ld_y, rows,
+        _stream(stream)),
+        "lemo_checkpoint_restore")
 
 
 def lemo_gated_mlp(gate, up, kept_total, pad_to, a, gate_checkpoint=None, up_checkpoint=None,
                    stream=None, d=None):
     """gate, up, a bf16 [rows, >= d]; a = SiLU(gate) up."""
     fit = _Fit("lemo_gated_mlp")
-    d = a.shape[1] if d is None else d
-    rows = a.shape[0]
-    kp = fit.total(kept_total)
+    rows, width = a.shape
+    d = width if d is None else int(d)
+    gp, ld_g = fit.mat(gate, "gate", _BF16, d, rows)
+    up_, ld_u = fit.mat(up, "up", _BF16, d, rows)
+    ap, ld_a = fit.mat(a, "a", _BF16, d)
     _check(load().lemo_gated_mlp(
-        fit.mat(gate, "gate", _BF16, d, rows), _ld(gate), fit.mat(up, "up", _BF16, d, rows),
-        _ld(up), int(d), kp, int(pad_to), fit.mat(a, "a", _BF16, d), _ld(a), rows,
+        gp, ld_g, up_, ld_u, d, fit.total(kept_total), pad_to, ap, ld_a, rows,
         fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
         fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), _stream(stream)),
         "lemo_gated_mlp")
@@ -551,25 +560,28 @@ def lemo_gated_mlp_backward(gate_checkpoint, up_checkpoint, da, kept_total, pad_
     """da, dgate, dup and the optional recomputed activation a: bf16 [rows, >= d]."""
     fit = _Fit("lemo_gated_mlp_backward")
     d, rows = gate_checkpoint.d, dgate.shape[0]
-    kp = fit.total(kept_total)
+    dap, ld_da = fit.mat(da, "da", _BF16, d, rows)
+    dgp, ld_dg = fit.mat(dgate, "dgate", _BF16, d)
+    dup_, ld_du = fit.mat(dup, "dup", _BF16, d, rows)
+    ap, ld_a = (None, 0) if a is None else fit.mat(a, "a", _BF16, d, rows)
     _check(load().lemo_gated_mlp_backward(
         fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
-        fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), fit.mat(da, "da", _BF16, d, rows),
-        _ld(da), kp, int(pad_to), fit.mat(dgate, "dgate", _BF16, d), _ld(dgate),
-        fit.mat(dup, "dup", _BF16, d, rows), _ld(dup),
-        None if a is None else fit.mat(a, "a", _BF16, d, rows), _ld(a), rows, _stream(stream)),
+        fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), dap, ld_da, fit.total(kept_total),
+        pad_to, dgp, ld_dg, dup_, ld_du, ap, ld_a, rows, _stream(stream)),
         "lemo_gated_mlp_backward")
 
 
 def lemo_checkpoint_weight_grad(checkpoint, dy, kept_total, dw, stream=None, n=None):
     """dw fp32 [n, >= d] += dy^T xhat; dy bf16 [rows, >= n], n = dy's width."""
     fit = _Fit("lemo_checkpoint_weight_grad")
-    d, rows = checkpoint.d, dy.shape[0]
-    n = dy.shape[1] if n is None else n
-    kp = fit.total(kept_total)
+    d = checkpoint.d
+    rows, width = dy.shape
+    n = width if n is None else int(n)
+    dyp, ld_dy = fit.mat(dy, "dy", _BF16, n)
+    dwp, ld_dw = fit.mat(dw, "dw", _FP32, d, n, 4)
     _check(load().lemo_checkpoint_weight_grad(
-        fit.ckpt(checkpoint, "checkpoint", d, rows), fit.mat(dy, "dy", _BF16, n), _ld(dy), rows,
-        int(n), kp, fit.mat(dw, "dw", _FP32, d, n), _ld(dw, 4), _stream(stream)),
+        fit.ckpt(checkpoint, "checkpoint", d, rows), dyp, ld_dy, rows, n, fit.total(kept_total),
+        dwp, ld_dw, _stream(stream)),
         "lemo_checkpoint_weight_grad")
 
 
