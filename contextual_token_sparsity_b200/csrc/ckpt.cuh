@@ -323,18 +323,46 @@ struct GatedArgs {
     View cg, cu;
 };
 
-// 1 / (1 + e^-g) from e^-|g| <= 1, so that nothing overflows for large -g.
-__device__ __forceinline__ float sigmoid(float g) {
-    const float t = __expf(-fabsf(g));
-    return __fdividef(g >= 0.f ? 1.f : t, 1.f + t);
-}
+// 1 / (1 + e^-g) of a pair, from t = e^-|g| <= 1 so that nothing overflows for
+// large -g.  t is the square of e^(-|g| / 2): the hardware exponential flushes
+// results below 2^-126 to 0, the square reaches the subnormals.  1 + t is in
+// [1, 2], where the hardware reciprocal needs no scaling.
 __device__ __forceinline__ F2 sigmoid2(F2 g) {
+    constexpr float kHalfLog2e = 0.72134752f;
     const float2 v = unf2(g);
-    return f2(sigmoid(v.x), sigmoid(v.y));
+    float tx, ty, rx, ry;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(tx) : "f"(fabsf(v.x) * -kHalfLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ty) : "f"(fabsf(v.y) * -kHalfLog2e));
+    const F2 half = f2(tx, ty), t = mul2(half, half);
+    const float2 d = unf2(add2(t, two(1.f))), e = unf2(t);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
+    return mul2(f2(v.x >= 0.f ? 1.f : e.x, v.y >= 0.f ? 1.f : e.y), f2(rx, ry));
 }
 
 // A warp takes 32 vectors of a row at a time, kPairs of them in flight.
 constexpr int kPairs = 2;
+
+// Item w of a grid of warps is chunk w % chunks of row w / chunks; a warp's next
+// item is nwarps further.
+struct Walk {
+    int64_t r, dr;
+    int c, dc, chunks;
+    __device__ __forceinline__ Walk(int64_t w, int64_t nwarps, int n) : chunks(n) {
+        r = w / n;
+        c = (int)(w - r * n);
+        dr = nwarps / n;
+        dc = (int)(nwarps - dr * n);
+    }
+    __device__ __forceinline__ void next() {
+        r += dr;
+        c += dc;
+        if (c >= chunks) {
+            c -= chunks;
+            ++r;
+        }
+    }
+};
 
 __global__ void __launch_bounds__(kThreads, 4) gated_kernel(const GatedArgs p) {
     pdl_entry();
@@ -342,17 +370,17 @@ __global__ void __launch_bounds__(kThreads, 4) gated_kernel(const GatedArgs p) {
     const int64_t K_pad = clamp_pad(K, p.pad_to, p.rows);
     const int lane = threadIdx.x & 31;
     const int chunks = (p.dvec + 31) / 32;
-    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5, items = K_pad * chunks;
-    for (int64_t w0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w0 < items;
-         w0 += kPairs * nwarps) {
+    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
+    Walk at(((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5, nwarps, chunks);
+    while (at.r < K_pad) {
         int64_t r[kPairs];
         int c[kPairs];
         uint4 g[kPairs], u[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
-            const int64_t w = w0 + k * nwarps;
-            r[k] = w < items ? w / chunks : K_pad;
-            c[k] = (int)(w - r[k] * chunks) * 32 + lane;
+            r[k] = at.r;
+            c[k] = at.c * 32 + lane;
+            at.next();
             g[k] = u[k] = make_uint4(0u, 0u, 0u, 0u);
             if (r[k] < K && c[k] < p.dvec) {
                 g[k] = __ldg(p.g + r[k] * p.ld_g + c[k]);
@@ -393,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 4) gated_backward_kernel(const Gated
     const int64_t K_pad = clamp_pad(K, p.pad_to, p.rows);
     const int lane = threadIdx.x & 31;
     const int chunks = (p.dvec + 31) / 32;
-    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5, items = K_pad * chunks;
-    for (int64_t w0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w0 < items;
-         w0 += kPairs * nwarps) {
+    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
+    Walk at(((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5, nwarps, chunks);
+    while (at.r < K_pad) {
         int64_t r[kPairs];
         int c[kPairs];
         uint4 da[kPairs];
@@ -403,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 4) gated_backward_kernel(const Gated
         uint32_t sg[kPairs], su[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
-            const int64_t w = w0 + k * nwarps;
-            r[k] = w < items ? w / chunks : K_pad;
-            c[k] = (int)(w - r[k] * chunks) * 32 + lane;
+            r[k] = at.r;
+            c[k] = at.c * 32 + lane;
+            at.next();
             da[k] = make_uint4(0u, 0u, 0u, 0u);
             qg[k] = qu[k] = make_uint2(0u, 0u);  // a row of the tail: zeros
             sg[k] = su[k] = 127u;
