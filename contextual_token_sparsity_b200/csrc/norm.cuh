@@ -659,8 +659,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             ph ^= 1;
         }
     }
-    if (!a.part || blockIdx.x >= K) return;
-    // column sums of this CTA: its groups in order, through the ring (every copy was consumed)
+    if (!a.part) return;
+    // column sums of this CTA (zeros where it had no row): its groups in order, through the ring (every copy was consumed)
     float f1[8 * V], f2s[FULL ? 8 * V : 1];
 #pragma unroll
     for (int j = 0; j < 4 * V; ++j) {
@@ -714,9 +714,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 
 struct SumArgs {
     const float* part;  // [parts][2][d]
-    int d, max_parts, second;  // second: the sums of dy (dn) are there too
-    const int32_t* kept_total;
-    int64_t rows;
+    int d, parts, second;  // second: the sums of dy (dn) are there too
     const uint16_t* w;     // of dgate
     const uint16_t* b;
     const uint16_t* gate;  // per channel, or nullptr
@@ -732,27 +730,33 @@ __device__ __forceinline__ float bf(const uint16_t* p, int c, float other) {
 }
 
 // Adds the CTAs' column sums in CTA order within 32 slices, then the slices in
-// order.  A thread's loads are issued kSumBatch rows at a time: 148 CTAs are one
-// batch per thread, so the kernel is one memory latency long, not five.
+// order.  All loads are independent and a thread's are issued kSumBatch rows at a
+// time (148 CTAs are one batch), so the kernel is one memory latency long.
 __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sums_kernel(const SumArgs a) {
     pdl_entry();
     __shared__ float2 acc[kSumSlices][kSumCols];
-    int64_t K = *a.kept_total;
-    if (K > a.rows) K = a.rows;
-    if (K <= 0) return;
-    const int parts = K < a.max_parts ? (int)K : a.max_parts;
     const int col = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
     const int c = blockIdx.x * kSumCols + col;
+    const bool last = slice == 0 && c < a.d;  // the thread that adds column c up
+    float dw = 0.f, db = 0.f, dg = 0.f, gate = 1.f, w = 1.f, b = 0.f;
+    if (last) {
+        if (a.dw) dw = a.dw[c];
+        if (a.db) db = a.db[c];
+        if (a.dgate) dg = a.dgate[c];
+        gate = bf(a.gate, c, 1.f);
+        w = bf(a.w, c, 1.f);
+        b = bf(a.b, c, 0.f);
+    }
     float2 s = make_float2(0.f, 0.f);
     if (c < a.d) {
-        for (int p0 = slice; p0 < parts; p0 += kSumSlices * kSumBatch) {
+        for (int p0 = slice; p0 < a.parts; p0 += kSumSlices * kSumBatch) {
             float x[kSumBatch], y[kSumBatch];
 #pragma unroll
             for (int j = 0; j < kSumBatch; ++j) {
                 const int p = p0 + j * kSumSlices;
                 const float* row = a.part + (int64_t)p * 2 * a.d;
-                x[j] = p < parts ? row[c] : 0.f;
-                y[j] = p < parts && a.second ? row[a.d + c] : 0.f;
+                x[j] = p < a.parts ? row[c] : 0.f;
+                y[j] = p < a.parts && a.second ? row[a.d + c] : 0.f;
             }
 #pragma unroll
             for (int j = 0; j < kSumBatch; ++j) {
@@ -763,16 +767,15 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sums_kernel(cons
     }
     acc[slice][col] = s;
     __syncthreads();
-    if (slice != 0 || c >= a.d) return;
+    if (!last) return;
 #pragma unroll
     for (int j = 1; j < kSumSlices; ++j) {
         s.x += acc[j][col].x;
         s.y += acc[j][col].y;
     }
-    const float gate = bf(a.gate, c, 1.f);
-    if (a.dw) a.dw[c] += gate * s.x;
-    if (a.db) a.db[c] += gate * s.y;
-    if (a.dgate) a.dgate[c] += bf(a.w, c, 1.f) * s.x + bf(a.b, c, 0.f) * s.y;
+    if (a.dw) a.dw[c] = dw + gate * s.x;
+    if (a.db) a.db[c] = db + gate * s.y;
+    if (a.dgate) a.dgate[c] = dg + (w * s.x + b * s.y);
 }
 
 }  // namespace norm

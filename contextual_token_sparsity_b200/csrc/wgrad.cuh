@@ -33,6 +33,13 @@
 // one tile are issued by one CTA pair, each accumulator's after those of the one
 // before have completed, so their order and the result are fixed.
 //
+// Few tiles leave most SMs idle while every pair walks over all rows.  Then the
+// rows of one item are split over the `splits` (2 or 4) pairs of a larger cluster,
+// accumulator by accumulator; the pairs add theirs into dW in turn, each after the
+// one before it has completed (a barrier in the next pair's CTA), so the order of
+// the adds stays fixed.  512 x 512 over 8192 rows: see the measurements at the
+// launch.
+//
 // Every wait is bounded in time; a wait that runs out records LEMO_ERR_TIMEOUT
 // and makes both CTAs of the pair drain what they issued, free their tensor
 // memory and return.
@@ -70,7 +77,6 @@ using score::tc_fence_after;
 using score::tc_fence_before;
 using score::tmem_ld16;
 using score::tmem_wait_ld;
-using score::umma_commit_pair;
 
 constexpr int TM = 256, TN = 256;   // output tile of a pair
 constexpr int HALF = 128;           // columns of each operand held by one CTA
@@ -99,6 +105,7 @@ struct Smem {
     uint64_t acc_full[2];        // each CTA: accumulator holds a finished chunk
     uint64_t acc_empty[2];       // leader: both CTAs' readers read an accumulator
     uint64_t done;               // each CTA: every MMA of the leader completed
+    uint64_t turn;               // each CTA: the adds before this CTA's next ones completed
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -115,6 +122,7 @@ struct Args {
     int n, d;
     int tiles_m;
     int whole, items;            // items below `whole` are 256 x 256 tiles, the others 256 x 128 halves
+    int splits;                  // pairs of a cluster; above 1 a cluster takes one item
     const int32_t* kept_total;
     int64_t rows;
     uint64_t spin_limit_ns;
@@ -179,6 +187,16 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
                  : "memory");
+}
+
+// Arrive once on this barrier in both CTAs of the pair when every MMA issued so
+// far by this thread has completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t pair_mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(pair_mask)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -285,14 +303,18 @@ __device__ __forceinline__ Item item_of(const Args& a, int i) {
 }
 
 template <int FORMAT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_dw,
                  const Args a) {
     pdl_entry();
     const int64_t K = ckpt::clamp_rows(a.kept_total, a.rows);
     const int kblocks = (int)((K + KB - 1) / KB);
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    if (kblocks == 0 || pair >= a.items) return;  // both CTAs of the pair leave together
+    const int splits = a.splits, split = (blockIdx.x >> 1) % splits;
+    const int cluster = blockIdx.x / (2 * splits), nclusters = gridDim.x / (2 * splits);
+    if (kblocks == 0 || cluster >= a.items) return;  // the whole cluster leaves together
+    // stages of one accumulator; split s takes accumulators s, s + splits, ...
+    const int chunk_kb = splits == 1 ? CHUNK : max(1, min(CHUNK, (kblocks + splits - 1) / splits));
+    const int next_kb = splits * chunk_kb;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -300,7 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Smem* sm = reinterpret_cast<Smem*>(base + OFF_BAR);
     const uint32_t sbase = smem_u32(base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cta_rank();
+    const uint32_t crank = cta_rank(), rank = crank & 1u, leader_rank = crank & ~1u;
+    const uint16_t pair_mask = (uint16_t)(3u << leader_rank);
     const bool leader = rank == 0;
     const uint64_t lim = a.spin_limit_ns;
 
@@ -315,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mbar_init(&sm->acc_empty[b], 2 * READERS);
         }
         mbar_init(&sm->done, 1);
+        mbar_init(&sm->turn, READERS);
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -329,16 +353,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = sm->tmem_base;
 
+    // the stage behind kb among those of this split
+    auto after = [&](int kb) { return (kb + 1) % chunk_kb ? kb + 1 : kb + 1 + next_kb - chunk_kb; };
+
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             uint32_t it = 0, s = 0, ph = 0;  // stage, its slot and the slot's phase
             bool ok = true;
-            for (int i = pair; ok && i < a.items; i += npairs) {
+            for (int i = cluster; ok && i < a.items; i += nclusters) {
                 const Item im = item_of(a, i);
                 if (im.width == 0) continue;
                 const int n0 = im.n0 + (int)rank * HALF;
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                for (int kb = split * chunk_kb; kb < kblocks; kb = after(kb), ++it) {
                     if (!(ok = wait(&sm->used[s], ph ^ 1, sm, lim))) break;
                     const uint32_t sa = sbase + s * A_BYTES;
                     mbar_arrive_expect_tx(&sm->a_full[s], A_BYTES);
@@ -362,12 +389,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ dy tiles for the leader
-        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), 0);
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), leader_rank);
         uint32_t s = 0, ph = 0;
         bool ok = true;
-        for (int i = pair; ok && i < a.items; i += npairs) {
+        for (int i = cluster; ok && i < a.items; i += nclusters) {
             if (item_of(a, i).width == 0) continue;
-            for (int kb = 0; kb < kblocks; ++kb) {
+            for (int kb = split * chunk_kb; kb < kblocks; kb = after(kb)) {
                 if (!(ok = wait_warp(&sm->a_full[s], ph, sm, lim))) break;
                 const int valid = (int)min((int64_t)KB, K - (int64_t)kb * KB);
                 if (valid < KB) {
@@ -398,14 +425,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // tested for in the middle of this one's MMAs, and waited for only if that failed.
             uint32_t s = 0, ready_ph = 0, buf = 0, empty_ph = 1;
             bool ok = true, seen = false;  // seen: `ready` of the stage at hand was observed
-            for (int i = pair; ok && i < a.items; i += npairs) {
+            for (int i = cluster; ok && i < a.items; i += nclusters) {
                 const Item im = item_of(a, i);
                 if (im.width == 0) continue;
                 const uint32_t id = im.width == TN ? idesc(TN) : idesc(HALF);
-                for (int k0 = 0; ok && k0 < kblocks; k0 += CHUNK) {
+                for (int k0 = split * chunk_kb; ok && k0 < kblocks; k0 += next_kb) {
                     if (!(ok = wait(&sm->acc_empty[buf], empty_ph, sm, lim))) break;
                     const uint32_t d_tmem = tmem_base + buf * TN;
-                    const int k1 = min(k0 + CHUNK, kblocks);
+                    const int k1 = min(k0 + chunk_kb, kblocks);
                     for (int kb = k0; kb < k1; ++kb) {
                         const uint64_t da = da0 + s * (A_BYTES >> 4), db = db0 + s * (B_BYTES >> 4);
                         if (!seen && !(ok = wait(&sm->ready[s], ready_ph, sm, lim))) break;
@@ -418,15 +445,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         seen = mbar_test(&sm->ready[s], ready_ph);
                         umma_pair(d_tmem, da + 2 * (2048 >> 4), db + 2 * (2048 >> 4), id, 1u);
                         umma_pair(d_tmem, da + 3 * (2048 >> 4), db + 3 * (2048 >> 4), id, 1u);
-                        umma_commit_pair(&sm->used[used_now]);
+                        umma_commit_pair(&sm->used[used_now], pair_mask);
                     }
                     if (!ok) break;
-                    umma_commit_pair(&sm->acc_full[buf]);
+                    umma_commit_pair(&sm->acc_full[buf], pair_mask);
                     buf ^= 1;
                     empty_ph ^= buf == 0 ? 1u : 0u;
                 }
             }
-            umma_commit_pair(&sm->done);
+            umma_commit_pair(&sm->done, pair_mask);
         }
         if (lane == 0) {
             // bounded: every MMA the leader issued completes before TMEM is freed
@@ -442,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------------ workers
         const int w = (warp - FIRST_WORKER) / 4 * 3 + (warp % 4 ? warp % 4 - 1 : 0);  // 0 .. 11
         const int team = w / TEAM, q = w % TEAM;
-        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), 0);
+        const uint32_t ready_c = map_to_rank(smem_u32(&sm->ready[0]), leader_rank);
         const int64_t turn_scales = (int64_t)TEAMS * KB * a.c.ld_scales;
         const int64_t turn_data = (int64_t)TEAMS * KB * a.c.ld;
         const int full_blocks = (int)(K / KB);
@@ -450,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         uint32_t turn = 0;        // stages this team has taken: stage = team + TEAMS turn
         uint32_t it = 0;          // stages before this item
         bool ok = true;
-        for (int i = pair; ok && i < a.items; i += npairs) {
+        for (int i = cluster; ok && i < a.items; i += nclusters) {
             const Item im = item_of(a, i);
             if (im.width == 0) continue;
             const bool wide = im.width == TN;
@@ -497,79 +524,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             };
             const int col = im.c0 + (int)rank * (im.width / 2) + 16 * chunk;
             const bool in = col < a.d;
-            int kb = (int)((team + TEAMS - it % TEAMS) % TEAMS);    // this team's next stage
-            const int64_t first = (int64_t)kb * KB + row0;
-            const uint8_t* sp = a.c.scales + (in ? col / ckpt::kGroup : 0) + first * a.c.ld_scales;
-            const uint8_t* dp = a.c.data + (in ? col : 0) + first * a.c.ld;
-            const int64_t step_scales = gap * a.c.ld_scales, step_data = gap * a.c.ld;
-            int left = (int)K - kb * KB - row0;  // rows from this lane's first
-            uint4 val[STEPS];       // codes and scale bytes of the team's next stage
-            uint32_t codes[STEPS];
-            // (columns past d are read from column 0: whatever they become is not stored)
-            auto load = [&]() {
-                if (kb < full_blocks) {
+            // a run of consecutive stages: all of them, or one accumulator's
+            for (int run = split * chunk_kb; ok && run < kblocks; run += next_kb) {
+                const int run_end = splits == 1 ? kblocks : min(run + chunk_kb, kblocks);
+                int kb = run + (int)((team + TEAMS - it % TEAMS) % TEAMS);    // this team's next stage
+                const int64_t first = (int64_t)kb * KB + row0;
+                const uint8_t* sp = a.c.scales + (in ? col / ckpt::kGroup : 0) + first * a.c.ld_scales;
+                const uint8_t* dp = a.c.data + (in ? col : 0) + first * a.c.ld;
+                const int64_t step_scales = gap * a.c.ld_scales, step_data = gap * a.c.ld;
+                int left = (int)K - kb * KB - row0;  // rows from this lane's first
+                uint4 val[STEPS];       // codes and scale bytes of the team's next stage
+                uint32_t codes[STEPS];
+                // (columns past d are read from column 0: whatever they become is not stored)
+                auto load = [&]() {
+                    if (kb < full_blocks) {
+#pragma unroll
+                        for (int j = 0; j < STEPS; ++j) {
+                            if (j >= STEPS / 2 && !wide) break;
+                            val[j] = __ldg(reinterpret_cast<const uint4*>(dp + j * step_data));
+                            codes[j] = __ldg(sp + j * step_scales);
+                        }
+                        return;
+                    }
 #pragma unroll
                     for (int j = 0; j < STEPS; ++j) {
-                        if (j >= STEPS / 2 && !wide) break;
-                        val[j] = __ldg(reinterpret_cast<const uint4*>(dp + j * step_data));
-                        codes[j] = __ldg(sp + j * step_scales);
+                        const bool on = gap * j < left && (wide || j < STEPS / 2);
+                        val[j] = on ? __ldg(reinterpret_cast<const uint4*>(dp + j * step_data)) : make_uint4(0u, 0u, 0u, 0u);
+                        codes[j] = on ? __ldg(sp + j * step_scales) : 3u;
                     }
-                    return;
-                }
-#pragma unroll
-                for (int j = 0; j < STEPS; ++j) {
-                    const bool on = gap * j < left && (wide || j < STEPS / 2);
-                    val[j] = on ? __ldg(reinterpret_cast<const uint4*>(dp + j * step_data)) : make_uint4(0u, 0u, 0u, 0u);
-                    codes[j] = on ? __ldg(sp + j * step_scales) : 3u;
-                }
-            };
-            load();
-            for (; kb < kblocks; ++turn) {
-                // the MMAs of the stage STAGES before have read the slot
-                const uint32_t s = team + (turn & 1) * TEAMS;
-                if (!(ok = wait_warp(&sm->used[s], ((turn >> 1) & 1) ^ 1, sm, lim))) break;
-                const uint32_t bt = sbase + OFF_B + s * B_BYTES;
-                uint32_t most = 0;
-#pragma unroll
-                for (int j = 0; j < STEPS; ++j)
-                    if (wide || j < STEPS / 2) most = max(most, codes[j]);
-                const bool one = kb < full_blocks && !__any_sync(0xffffffffu, most > kOneFactor);
-                if (wide && one)
-                    convert(std::true_type{}, std::true_type{}, bt, left, val, codes);
-                else if (wide)
-                    convert(std::true_type{}, std::false_type{}, bt, left, val, codes);
-                else if (one)
-                    convert(std::false_type{}, std::true_type{}, bt, left, val, codes);
-                else
-                    convert(std::false_type{}, std::false_type{}, bt, left, val, codes);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
-                sp += turn_scales;
-                dp += turn_data;
-                left -= TEAMS * KB;
-                kb += TEAMS;
+                };
                 load();
+                for (; kb < run_end; ++turn) {
+                    // the MMAs of the stage STAGES before have read the slot
+                    const uint32_t s = team + (turn & 1) * TEAMS;
+                    if (!(ok = wait_warp(&sm->used[s], ((turn >> 1) & 1) ^ 1, sm, lim))) break;
+                    const uint32_t bt = sbase + OFF_B + s * B_BYTES;
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int j = 0; j < STEPS; ++j)
+                        if (wide || j < STEPS / 2) most = max(most, codes[j]);
+                    const bool one = kb < full_blocks && !__any_sync(0xffffffffu, most > kOneFactor);
+                    if (wide && one)
+                        convert(std::true_type{}, std::true_type{}, bt, left, val, codes);
+                    else if (wide)
+                        convert(std::true_type{}, std::false_type{}, bt, left, val, codes);
+                    else if (one)
+                        convert(std::false_type{}, std::true_type{}, bt, left, val, codes);
+                    else
+                        convert(std::false_type{}, std::false_type{}, bt, left, val, codes);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ready_c + s * 8);
+                    sp += turn_scales;
+                    dp += turn_data;
+                    left -= TEAMS * KB;
+                    kb += TEAMS;
+                    load();
+                }
+                it += (uint32_t)(run_end - run);
+                if (splits == 1) break;
             }
-            it += (uint32_t)kblocks;
         }
     } else if (warp >= FIRST_READER) {
         // ------------------------------------------------------------ accumulator readers
         const int q = warp & 3;  // TMEM lane quadrant
         const uint32_t lane_addr = tmem_base + ((uint32_t)(q * 32) << 16);
         const uint32_t my_stg = sbase + OFF_STG + (warp - FIRST_READER) * 2 * STG_BYTES;
-        const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), 0);
-        uint32_t buf = 0, full_ph = 0;
+        const uint32_t empty_c = map_to_rank(smem_u32(&sm->acc_empty[0]), leader_rank);
+        // the same CTA of the next pair: its adds come after these
+        const uint32_t turn_c = map_to_rank(smem_u32(&sm->turn), (crank + 2) % (2 * splits));
+        uint32_t buf = 0, full_ph = 0, turn_ph = 0;
         bool ok = true;
-        for (int i = pair; ok && i < a.items; i += npairs) {
+        for (int i = cluster; ok && i < a.items; i += nclusters) {
             const Item im = item_of(a, i);
             if (im.width == 0) continue;
             const int out_n = im.n0 + (int)rank * HALF + q * 32;
-            for (int k0 = 0; k0 < kblocks; k0 += CHUNK) {
+            for (int k0 = split * chunk_kb; k0 < kblocks; k0 += next_kb) {
                 if (!(ok = wait_warp(&sm->acc_full[buf], full_ph, sm, lim))) break;
                 tc_fence_after();
-                // adds of the accumulator before have completed: one element's adds keep their order
+                // The adds of the accumulator before have completed (this warp's own, or those
+                // of the pair before): one element's adds keep their order.
                 if (lane == 0) bulk_wait_all();
+                if (splits > 1 && k0 > 0) {
+                    if (!(ok = wait_warp(&sm->turn, turn_ph, sm, lim))) break;
+                    turn_ph ^= 1;
+                }
 #pragma unroll 1
                 for (int ch = 0; ch < im.width; ch += BOX) {
                     uint32_t r[BOX];
@@ -598,6 +637,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             tma_reduce_add_2d(&tm_dw, box, im.c0 + ch, out_n);
                         bulk_commit();
                     }
+                }
+                if (splits > 1 && k0 + chunk_kb < kblocks && lane == 0) {
+                    bulk_wait_all();
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(turn_c)
+                                 : "memory");
                 }
                 buf ^= 1;
                 full_ph ^= buf == 0 ? 1u : 0u;

@@ -184,6 +184,27 @@ def test_weight_grad_rows(K):
     check_wgrad(K, 264, 272, ["e4m3", "int8"][K % 2])
 
 
+@pytest.mark.parametrize("K", [0, 1, 64, 100, 700, 2047, 2048, 5000, 8192])
+def test_weight_grad_rows_split_over_a_cluster(K):
+    """Few tiles and room for many rows: the rows of a tile are split over two or four CTA
+    pairs, whatever the device's row count turns out to be."""
+    check_wgrad(K, 512, 264, ["int8", "e4m3"][K % 2], rows=8192)
+    check_wgrad(min(K, 1500), 136, 72, "e4m3", rows=1500)
+
+
+def test_weight_grad_split_is_deterministic():
+    rng = np.random.default_rng(6)
+    K, n, d = 8192, 512, 512
+    ck, _, _ = make_ckpt(K, d, "e4m3")
+    lemo.lemo_checkpoint_save(bf16(draw(rng, K, d)), None, dev_i32(K), ck)
+    dy = bf16(draw(rng, K, n))
+    runs = [torch.zeros(n, d, device="cuda") for _ in range(4)]
+    for dw in runs:
+        lemo.lemo_checkpoint_weight_grad(ck, dy, dev_i32(K), dw)
+    ok()
+    assert all(torch.equal(runs[0], dw) for dw in runs[1:])
+
+
 def test_weight_grad_many_tiles():
     check_wgrad(200, 2056, 2600, "e4m3")
 
@@ -214,15 +235,17 @@ def test_weight_grad_accumulates_and_is_deterministic():
     rng = np.random.default_rng(4)
     K, n, d = 1500, 520, 776
     ck, _, _ = make_ckpt(K, d, "int8")
-    lemo.lemo_checkpoint_save(bf16(draw(rng, K, d)), None, dev_i32(K), ck)
-    dy = bf16(draw(rng, K, n))
+    v, g = draw(rng, K, d), draw(rng, K, n)
+    lemo.lemo_checkpoint_save(bf16(v), None, dev_i32(K), ck)
+    dy = bf16(g)
     one, two = torch.zeros(n, d, device="cuda"), torch.zeros(n, d, device="cuda")
-    lemo.lemo_checkpoint_weight_grad(ck, dy, dev_i32(K), one)
-    lemo.lemo_checkpoint_weight_grad(ck, dy, dev_i32(K), two)
-    assert torch.equal(one, two)
-    lemo.lemo_checkpoint_weight_grad(ck, dy, dev_i32(K), two)
-    assert torch.equal(2 * one, two)
+    for dw in (one, two, one, two):
+        lemo.lemo_checkpoint_weight_grad(ck, dy, dev_i32(K), dw)
     ok()
+    assert torch.equal(one, two)
+    q, _ = so.checkpoint_codes(v, "int8")
+    # two sums of K terms (check_wgrad's bound each) and their additions, which the K + 8 covers
+    within(f64(one), 2 * so.weight_grad(g, q), 2 * 2 * (K + 8) * U32 * (np.abs(g).T @ np.abs(q)))
 
 
 def test_too_many_rows_are_reported():
