@@ -300,7 +300,7 @@ def lemo_segment_loss(h, w, targets, seg_rows, loss, ws, token_loss=None, dh=Non
 # the current CUDA device and has the type, row layout and sizes the call
 # needs; a tensor that does not fit raises LemoError(LEMO_ERR_INVALID_ARG).
 # ---------------------------------------------------------------------------
-_BF16 = _FP32 = _INT32 = _UINT8 = None  # torch dtypes, set with the first _Fit
+_torch = _BF16 = _FP32 = _INT32 = _UINT8 = None  # torch and its dtypes, set with the first _Fit
 
 
 class _Fit:
@@ -368,15 +368,16 @@ class _Fit:
 
 
 def _bind_torch():
-    global _BF16, _FP32, _INT32, _UINT8
+    global _torch, _BF16, _FP32, _INT32, _UINT8
     import torch
+    _torch = torch
     _BF16, _FP32, _INT32, _UINT8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _device() -> int:
     """Current CUDA device, or -2 where CUDA is not in use (no tensor is on it)."""
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    cuda = _torch.cuda
+    return cuda.current_device() if cuda.is_initialized() else -2
 
 
 class Checkpoint:

@@ -8,6 +8,13 @@ needs for a fixed batch layout and exposes the steps in order:
     layer.gather(x)            y = x[kept] + zero tail     (lemo_gather_pad)
     layer.scatter(x, y_out)    x[kept] += y_out, in place  (lemo_scatter_residual)
 
+A sublayer with norms takes, in place of the last two, the forms that fuse
+them with the movement, and their backward passes:
+
+    layer.gather_norm(...)     y = norm(x[kept]) w + b     (lemo_norm_gather)
+    layer.scatter_norm(...)    x[kept] += s gate norm(y)   (lemo_norm_scatter)
+    layer.checkpoint(...)      8-bit rows for one kept-row buffer (make_checkpoint)
+
 No step copies anything to the host; K stays on the device.
 """
 
@@ -76,6 +83,55 @@ class Layer:
         self.select(theta, stream)
         self.gather(x, stream)
         self.scatter(x, y_out, stream)
+
+    # -- norms around the sublayer, 8-bit checkpoints ---------------------------
+    def _norm_buffers(self):
+        """Statistics of both norms and the backward passes' workspace (first use allocates)."""
+        if not hasattr(self, "norm_ws"):
+            t, dev = self.torch, self.y.device
+            self.pre_stats = t.empty((self.y_rows, 2), dtype=t.float32, device=dev)
+            self.post_stats = t.empty((self.y_rows, 2), dtype=t.float32, device=dev)
+            self.norm_ws = t.empty(lemo.lemo_norm_workspace_size(self.d), dtype=t.uint8, device=dev)
+
+    def checkpoint(self, format: int, width: int | None = None):
+        """An empty checkpoint for a kept-row buffer of `width` columns (d by default)."""
+        t, dev, d = self.torch, self.y.device, self.d if width is None else width
+        return lemo.make_checkpoint(
+            t.empty((self.y_rows, _round_up(d, 16)), dtype=t.uint8, device=dev),
+            t.empty((self.y_rows, _round_up(-(-d // 32), 4)), dtype=t.uint8, device=dev), format, d)
+
+    def gather_norm(self, norm, x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None,
+                    stream=None):
+        self._norm_buffers()
+        lemo.lemo_norm_gather(norm, x, weight, bias, eps, self.kept_idx, self.kept_total,
+                              self.pad_to, self.y, stats=self.pre_stats, checkpoint=checkpoint,
+                              stream=stream)
+        return self.y
+
+    def gather_norm_backward(self, norm, dy, dx, weight=None, x=None, checkpoint=None, dweight=None,
+                             dbias=None, stream=None):
+        """dx[kept] += d loss / d x[kept], in place, from the gradient dy of gather_norm's rows."""
+        lemo.lemo_norm_gather_backward(norm, dy, weight, self.pre_stats, self.kept_idx,
+                                       self.kept_total, dx, self.norm_ws, x=x,
+                                       checkpoint=checkpoint, dweight=dweight, dbias=dbias,
+                                       stream=stream)
+
+    def scatter_norm(self, norm, x, y_out, weight=None, bias=None, eps: float = 1e-5, gate=None,
+                     scale: float = 1.0, checkpoint=None, stream=None):
+        self._norm_buffers()
+        stats = None if norm == lemo.LEMO_NORM_NONE else self.post_stats
+        lemo.lemo_norm_scatter(norm, x, y_out, weight, bias, eps, gate, scale, self.kept_idx,
+                               self.kept_total, stats=stats, checkpoint=checkpoint, stream=stream)
+
+    def scatter_norm_backward(self, norm, dx, dy_out, weight=None, bias=None, gate=None,
+                              scale: float = 1.0, y_out=None, checkpoint=None, dweight=None,
+                              dbias=None, dgate=None, stream=None):
+        """dy_out = the gradient of scatter_norm's y_out, zero-padded; dx is only read."""
+        stats = None if norm == lemo.LEMO_NORM_NONE else self.post_stats
+        lemo.lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, self.kept_idx,
+                                        self.kept_total, self.pad_to, dy_out, self.norm_ws,
+                                        y=y_out, checkpoint=checkpoint, dweight=dweight,
+                                        dbias=dbias, dgate=dgate, stream=stream)
 
     # -- helpers for checking results ----------------------------------------
     def block_max_list(self):
