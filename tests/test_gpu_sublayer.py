@@ -224,3 +224,41 @@ def test_weight_grad_in_two_graphs():
         for t in dw:
             within(f64(t), want, 2 * (K + 8) * U32 * (np.abs(g[:K]).T @ np.abs(q[:K])))
     ok()
+
+
+def test_offsets_past_32_bits():
+    """Row strides that put the last rows more than 2^31 elements (2^32 bytes) behind the first."""
+    rng = np.random.default_rng(3)
+    d, ld, rows = 64, 1 << 17, 33000            # 33000 x 131072 = 4.3e9 elements
+    idx = np.array([0, 5, 16385, 32766, 32999], dtype=np.int32)
+    K = len(idx)
+    K_d, idx_d = torch.tensor([K], dtype=torch.int32, device="cuda"), torch.from_numpy(idx).cuda()
+    big = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda").as_strided((rows, d), (ld, 1))
+    v = draw(rng, K, d)
+    big[idx_d.long()] = bf16(v)
+    y = torch.zeros(K, d, dtype=torch.bfloat16, device="cuda")
+    stats = torch.zeros(K, 2, device="cuda")
+    lemo.lemo_norm_gather(RMS, big, None, None, EPS, idx_d, K_d, 1, y, stats=stats, d=d)
+    n, mean, rstd = so.norm_rows(v, "rms", EPS)
+    within(f64(y), n, U16 * np.abs(n) + 1.01 * norm_slop(v, mean, rstd, None, None), "y")
+    lemo.lemo_norm_scatter(lemo.LEMO_NORM_NONE, big, y, None, None, EPS, None, 1.0, idx_d, K_d, d=d)
+    got, yv = f64(big[idx_d.long()]), f64(y)
+    within(got, v + yv, U16 * np.abs(v + yv), "x")
+    # a checkpoint whose rows are as far apart, its kept rows the last ones
+    del big
+    whole = torch.empty(rows * ld, dtype=torch.uint8, device="cuda").as_strided((rows, d), (ld, 1))
+    c = lemo.make_checkpoint(whole, torch.zeros(rows, 4, dtype=torch.uint8, device="cuda"), 1, d)
+    x = bf16(draw(rng, rows, d))
+    R_d = torch.tensor([rows], dtype=torch.int32, device="cuda")
+    lemo.lemo_checkpoint_save(x, None, R_d, c)
+    back = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+    lemo.lemo_checkpoint_restore(c, R_d, 1, back)
+    ok()
+    want, _ = so.checkpoint_codes(f64(x[-40:]), "int8")
+    assert np.array_equal(f64(back[-40:]), want)
+    dy = bf16(draw(rng, rows, 8))
+    dw = torch.zeros(8, d, device="cuda")
+    lemo.lemo_checkpoint_weight_grad(c, dy, R_d, dw)
+    ok()
+    a, b = f64(dy), f64(back)
+    within(f64(dw), a.T @ b, 2 * (rows + 8) * U32 * (np.abs(a).T @ np.abs(b)), "dw")
