@@ -1244,10 +1244,13 @@ bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* gr
     return true;
 }
 
-// The group of threads that takes a row of dvec 16-byte vectors: one vector per
-// thread up to 640 threads, then 512 threads with two or four.  Rows per group and
-// stage: as many as keep at least two stages in the ring (a row is up to three
-// streams of 16 dvec bytes).
+// The group of threads that takes a row of dvec 16-byte vectors, the vectors of a
+// thread and the rows of a group and stage: enough rows at once to cover the
+// reduction's latency, few enough for two stages in the ring (a row is up to three
+// streams of 16 dvec bytes) and for the registers.  Measured at 8192 x 4096, us:
+// forward 256 x 2 x 2 32.8, 512 x 1 x 4 34.9, 512 x 1 x 2 40.9, 128 x 4 x 1 41.0;
+// backward with a mean and from codes 512 x 1 x 4 71.7, 256 x 2 x 2 92 (spills); at
+// 4096 x 8192 512 x 2 x 1 73.7, 512 x 2 x 2 92 (spills).
 template <bool BWD, bool POST, bool FULL, bool CODED>
 lemo_status run_norm_as(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     using lemo::norm::Shape;
@@ -1267,7 +1270,9 @@ lemo_status run_norm_as(lemo::norm::Args& a, cudaStream_t st, int* grid) {
         ok = launch_norm<BWD, POST, FULL, CODED, std::conditional_t<BWD && FULL, Shape<512, 1, 4>, Shape<256, 2, 2>>>(
             a, dev, sms, st, grid);
     else if (a.dvec <= 640) ok = launch_norm<BWD, POST, FULL, CODED, Shape<640, 1, 2>>(a, dev, sms, st, grid);
-    else if (a.dvec <= 1024) ok = launch_norm<BWD, POST, FULL, CODED, Shape<512, 2, 2>>(a, dev, sms, st, grid);
+    else if (a.dvec <= 1024)
+        ok = launch_norm<BWD, POST, FULL, CODED, std::conditional_t<BWD && FULL, Shape<512, 2, 1>, Shape<512, 2, 2>>>(
+            a, dev, sms, st, grid);
     else ok = launch_norm<BWD, POST, FULL, CODED, Shape<512, 4, 1>>(a, dev, sms, st, grid);
     const lemo_status e = launch_status();
     return ok ? e : LEMO_ERR_CUDA;
@@ -1297,6 +1302,7 @@ lemo_status run_column_sums(const lemo::norm::Args& n, int parts, const uint16_t
     s.d = n.d;
     s.parts = parts;
     s.second = second ? 1 : 0;
+    s.scale = n.scale;
     s.w = w;
     s.b = b;
     s.gate = gate;

@@ -13,7 +13,7 @@
 //
 // gather:   g = dy w;  dx[t] += dv;  dw += sum_r dy vhat;  db += sum_r dy
 // scatter:  dz = scale dx[t];  g = dz gate w;  dy[r] = dv;
-//           S1 = sum_r dz vhat, S2 = sum_r dz:  dw += gate S1, db += gate S2,
+//           S1 = scale sum_r dx vhat, S2 = scale sum_r dx:  dw += gate S1, db += gate S2,
 //           dgate += w S1 + b S2   (per-channel gate: three sums from two)
 //           a gate of one value per token and channel goes into S1 and S2, and
 //           its gradient rows are dz (vhat w + b).
@@ -477,10 +477,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
     int flip = 0;
-    uint4 w[V];
+    // Four vectors per thread leave no registers for the weights: they come from L1 then.
+    constexpr bool kHoldW = V <= 2;
+    uint4 w[kHoldW ? V : 1];
     F2 s1[4 * V], s2[FULL ? 4 * V : 1];
 #pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = ld_or(a.w, v * G + i, v * G + i < a.dvec, kOnes);
+    for (int v = 0; v < (kHoldW ? V : 1); ++v) w[v] = ld_or(a.w, v * G + i, v * G + i < a.dvec, kOnes);
+    auto weight = [&](int v, F2* f) {
+        unpack8(kHoldW ? w[kHoldW ? v : 0] : ld_or(a.w, v * G + i, true, kOnes), f);
+    };
 #pragma unroll
     for (int j = 0; j < 4 * V; ++j) {
         s1[j] = two(0.f);
@@ -542,18 +547,23 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
                 for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], two(m.y));
             }
         };
-        // gradient of the row's output (POST: of n, with the scale, before the gate)
+        // Gradient of the row's output (POST: dx).  The residual scale goes into rstd below and
+        // into the column sums at the end, a gate of one row into the weights.
         auto grad = [&](int q, int v, F2* f) {
             unpack8(ld_shared(row0 + q * a.slot + a.in[1].off + 16 * (v * G + i)), f);
-            if (POST) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], two(a.scale));
-            }
         };
-        auto gated = [&](int q, int v, F2* f) {
-            const int c = v * G + i;
-            unpack8(a.ld_gate ? ld_shared(row0 + q * a.slot + a.in[2].off + 16 * c)
-                              : ld_or(a.gate, c, true, kOnes), f);
+        auto token_gate = [&](int q, int v, F2* f) {
+            unpack8(ld_shared(row0 + q * a.slot + a.in[2].off + 16 * (v * G + i)), f);
+        };
+        // weights of vector v, times the gate of one row
+        auto weight_gate = [&](int v, F2* f) {
+            weight(v, f);
+            if (POST && a.ld_gate == 0 && a.gate) {
+                F2 gf[4];
+                unpack8(__ldg(a.gate + v * G + i), gf);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], gf[j]);
+            }
         };
         F2 p1[R], p2[R];
 #pragma unroll
@@ -563,40 +573,31 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             const int c = v * G + i;
             if (c >= a.dvec) continue;
             F2 wf[4];
-            unpack8(w[v], wf);
+            weight_gate(v, wf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 if (token[q] < 0) continue;  // no row: nothing goes into the sums
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 grad(q, v, gg);
-                if (POST) {
-                    F2 gf[4];
-                    gated(q, v, gf);
+                if (POST && a.ld_gate) {
                     if (a.dgate_rows) {
                         F2 bf[4];
                         unpack8(ld_or(a.b, c, true, 0u), bf);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) bf[j] = mul2(gg[j], fma2(vv[j], wf[j], bf[j]));
+                        for (int j = 0; j < 4; ++j)
+                            bf[j] = mul2(mul2(gg[j], two(a.scale)), fma2(vv[j], wf[j], bf[j]));
                         a.dgate_rows[row_of<S>(st, group * R + q) * a.ld_dgate + c] = pack8(bf);
                     }
+                    F2 gf[4];
+                    token_gate(q, v, gf);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const F2 dn = mul2(gg[j], gf[j]);
-                        const F2 sum = a.ld_gate ? dn : gg[j];
-                        s1[4 * v + j] = fma2(sum, vv[j], s1[4 * v + j]);
-                        if (FULL) s2[4 * v + j] = add2(s2[4 * v + j], sum);
-                        gg[j] = dn;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s1[4 * v + j] = fma2(gg[j], vv[j], s1[4 * v + j]);
-                        if (FULL) s2[4 * v + j] = add2(s2[4 * v + j], gg[j]);
-                    }
+                    for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], gf[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    s1[4 * v + j] = fma2(gg[j], vv[j], s1[4 * v + j]);
+                    if (FULL) s2[4 * v + j] = add2(s2[4 * v + j], gg[j]);
                     gg[j] = mul2(gg[j], wf[j]);
                     p1[q] = fma2(gg[j], vv[j], p1[q]);
                     if (FULL) p2[q] = add2(p2[q], gg[j]);
@@ -619,20 +620,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             const int c = v * G + i;
             if (c >= a.dvec) continue;
             F2 wf[4];
-            unpack8(w[v], wf);
+            weight_gate(v, wf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 if (token[q] < 0) continue;
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 grad(q, v, gg);
-                if (POST) {
+                if (POST && a.ld_gate) {
                     F2 gf[4];
-                    gated(q, v, gf);
+                    token_gate(q, v, gf);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], gf[j]);
                 }
-                const F2 rs = two(stats[q].y), c1 = two(p[q]), c2 = two(FULL ? p[P - R + q] : 0.f);
+                const F2 rs = two(POST ? stats[q].y * a.scale : stats[q].y), c1 = two(p[q]), c2 = two(FULL ? p[P - R + q] : 0.f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     gg[j] = fma2(vv[j], c1, mul2(gg[j], wf[j]));
@@ -715,6 +716,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 struct SumArgs {
     const float* part;  // [parts][2][d]
     int d, parts, second;  // second: the sums of dy (dn) are there too
+    float scale;           // of all sums
     const uint16_t* w;     // of dgate
     const uint16_t* b;
     const uint16_t* gate;  // per channel, or nullptr
@@ -773,6 +775,8 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices) column_sums_kernel(cons
         s.x += acc[j][col].x;
         s.y += acc[j][col].y;
     }
+    s.x *= a.scale;
+    s.y *= a.scale;
     if (a.dw) a.dw[c] = dw + gate * s.x;
     if (a.db) a.db[c] = db + gate * s.y;
     if (a.dgate) a.dgate[c] = dg + (w * s.x + b * s.y);
