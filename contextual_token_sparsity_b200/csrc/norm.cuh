@@ -68,6 +68,7 @@ struct Shape {
     static constexpr int kGroups = kConsumers / G;
     static constexpr int kWarps = G / 32;
     static constexpr int kRows = kGroups * R;         // rows of a stage
+    static constexpr bool kNarrow = G * V <= 128;     // rows of up to 1024 values
     static_assert(kRows <= kMaxRows && kConsumers / 32 <= kMaxWarps, "");
 };
 
@@ -213,15 +214,40 @@ __device__ __forceinline__ uint4 ld_or(const uint4* p, int c, bool in, uint32_t 
 }
 constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 
-// Row j of stage st of this CTA.
+// How K rows are dealt.  Narrow rows (up to 1024 values): a CTA takes `m`
+// neighbouring rows per stage (fewer than a stage holds when that is all there is
+// for every CTA), and a slot keeps the rows of a stream together, so that rows that
+// are neighbours in memory come with one copy: 16384 x 512 is bound by the number
+// of copies, 18.4 us forward against 16.4.  Wide rows go round the CTAs one by one,
+// each with its streams together: at 8192 x 5120 43 us forward so, 45 as above.
 template <typename S>
-__device__ __forceinline__ int64_t row_of(int64_t st, int j) {
-    return blockIdx.x + (st * S::kRows + j) * (int64_t)gridDim.x;
+struct Deal {
+    int64_t K;
+    int m;
+    __device__ __forceinline__ explicit Deal(int64_t k) : K(k) {
+        const int64_t share = (k + gridDim.x - 1) / gridDim.x;
+        m = S::kNarrow && share < S::kRows ? (int)share : S::kRows;
+    }
+    __device__ __forceinline__ int64_t row(int64_t st, int j) const {
+        return S::kNarrow ? (st * gridDim.x + blockIdx.x) * m + j
+                          : blockIdx.x + (st * S::kRows + j) * (int64_t)gridDim.x;
+    }
+    __device__ __forceinline__ bool any(int64_t st) const { return row(st, 0) < K; }
+    __device__ __forceinline__ bool has(int64_t st, int j) const { return j < m && row(st, j) < K; }
+};
+
+// Shared-memory address of stream k of row j in slot s.
+template <typename S>
+__device__ __forceinline__ uint32_t slot_addr(const Args& a, uint32_t ring, int s, int k, int j) {
+    if (S::kNarrow)
+        return ring + (uint32_t)(s * S::kRows) * a.slot + S::kRows * a.in[k].off + j * a.in[k].bytes;
+    return ring + (uint32_t)(s * S::kRows + j) * a.slot + a.in[k].off;
 }
 
-// The producer warp: lane j brings row j of a stage.
+// The producer warp: lane j brings row j of a stage; narrow rows that follow one
+// another in memory come with the first of them.
 template <typename S>
-__device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, int64_t K,
+__device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, const Deal<S>& deal,
                                         bool ascending, bool want_stats) {
     constexpr int NR = S::kRows;
     const int lane = threadIdx.x & 31;
@@ -229,12 +255,12 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
     uint32_t ph = 0;
     bool ok = true;
     int64_t st = 0;
-    for (; row_of<S>(st, 0) < K; ++st) {
+    for (; deal.any(st); ++st) {
         // this stage's tokens and statistics, read while the slot may still be in use
-        const int64_t r = row_of<S>(st, lane);
+        const int64_t r = deal.row(st, lane);
         int64_t t = -1;
         float2 stat = make_float2(0.f, 1.f);
-        if (lane < NR && r < K) {
+        if (deal.has(st, lane)) {
             t = a.kept_idx ? a.kept_idx[r] : r;
             bool good = t >= 0 && t < a.x_rows && t < a.src_rows;
             // two rows of one token would race in the kernels that update token rows
@@ -247,6 +273,11 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
         }
         if (!(ok = wait_warp(&sm->empty[s], ph ^ 1, sm, a.spin_limit_ns))) break;
         const uint32_t rows = __ballot_sync(0xffffffffu, t >= 0);
+        const int64_t t_before = __shfl_up_sync(0xffffffffu, t, 1);
+        // rows (of kept-row streams) and tokens that do not continue those of the lane before
+        const bool follows = lane > 0 && t >= 0 && ((rows >> (lane - 1)) & 1u);
+        const uint32_t breaks_r = __ballot_sync(0xffffffffu, !follows);
+        const uint32_t breaks_t = __ballot_sync(0xffffffffu, !(follows && t == t_before + 1));
         if (lane < NR) {
             sm->token[s][lane] = (int32_t)t;
             sm->stats[s][lane] = stat;
@@ -259,10 +290,18 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
         }
         __syncwarp();
         if (t >= 0) {
-            const uint32_t dst = ring + (uint32_t)(s * NR + lane) * a.slot;
-            for (int i = 0; i < a.streams; ++i)
-                bulk_load(dst + a.in[i].off, a.in[i].base + (a.in[i].by_token ? t : r) * a.in[i].ld,
-                          a.in[i].bytes, &sm->full[s]);
+            for (int i = 0; i < a.streams; ++i) {
+                const int64_t at = a.in[i].by_token ? t : r;
+                uint32_t bytes = a.in[i].bytes;
+                if (S::kNarrow && a.in[i].ld == bytes) {
+                    const uint32_t breaks = a.in[i].by_token ? breaks_t : breaks_r;
+                    if (!((breaks >> lane) & 1u)) continue;  // came with a row before
+                    const uint32_t rest = lane < 31 ? breaks >> (lane + 1) : 0u;
+                    bytes *= rest ? (uint32_t)__ffs(rest) : 32u - lane;
+                }
+                bulk_load(slot_addr<S>(a, ring, s, i, lane), a.in[i].base + at * a.in[i].ld, bytes,
+                          &sm->full[s]);
+            }
         }
         if (++s == a.stages) {
             s = 0;
@@ -307,7 +346,7 @@ __device__ __forceinline__ void zero_tail(const Args& a, int64_t K, int64_t K_pa
 // ---------------------------------------------------------------------------
 template <typename S, bool POST, bool FULL>
 __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_constant__ Args a) {
-    constexpr int G = S::G, V = S::V, R = S::R;
+    constexpr int G = S::G, V = S::V, R = S::R, NG = S::kGroups;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem* sm = reinterpret_cast<Smem*>(smem_raw);
     init_ring<S>(a, sm);
@@ -318,8 +357,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
         const int64_t K_pad = ckpt::clamp_pad(K, a.pad_to, a.rows);
         if (K_pad > K) zero_tail<S>(a, K, K_pad);
     }
+    const Deal<S> deal(K);
     if (threadIdx.x >= S::kConsumers) {
-        produce<S>(a, sm, ring, K, POST, false);
+        produce<S>(a, sm, ring, deal, POST, false);
         return;
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
@@ -334,18 +374,22 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
     }
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t st = 0; row_of<S>(st, 0) < K; ++st) {
+    for (int64_t st = 0; deal.any(st); ++st) {
         if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
-        const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
-        const int32_t* token = &sm->token[s][group * R];
+        // row q of this group is row q NG + group of the stage
+        const int32_t* tokens = &sm->token[s][group];
+        const uint32_t base0 = slot_addr<S>(a, ring, s, 0, group);
+        auto at = [&](int k, int q, int c) {  // vector c of stream k
+            return S::kNarrow ? slot_addr<S>(a, ring, s, k, q * NG + group) + 16 * c
+                              : base0 + a.in[k].off + q * (NG * a.slot) + 16 * c;
+        };
         uint4 in[R][V];
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = v * G + i;
-                in[q][v] = token[q] >= 0 && c < a.dvec ? ld_shared(row0 + q * a.slot + 16 * c)
-                                                       : make_uint4(0u, 0u, 0u, 0u);
+                in[q][v] = tokens[q * NG] >= 0 && c < a.dvec ? ld_shared(at(0, q, c)) : make_uint4(0u, 0u, 0u, 0u);
             }
         float mean[R], rstd[R];
 #pragma unroll
@@ -396,14 +440,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
         if (a.stats && i == 0) {
 #pragma unroll
             for (int q = 0; q < R; ++q)
-                if (token[q] >= 0) a.stats[row_of<S>(st, group * R + q)] = make_float2(mean[q], rstd[q]);
+                if (tokens[q * NG] >= 0) a.stats[deal.row(st, q * NG + group)] = make_float2(mean[q], rstd[q]);
         }
         uint4* out[R];
         uint8_t *data[R], *scales[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t r = row_of<S>(st, group * R + q);
-            out[q] = POST ? a.x + (int64_t)token[q] * a.ld_x : a.y + r * a.ld_y;
+            const int64_t r = deal.row(st, q * NG + group);
+            out[q] = POST ? a.x + (int64_t)tokens[q * NG] * a.ld_x : a.y + r * a.ld_y;
             data[q] = a.c.data + r * a.c.ld;
             scales[q] = a.c.scales + r * a.c.ld_scales;
         }
@@ -415,7 +459,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
             if (FULL) unpack8(b[v], bf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                if (token[q] < 0) continue;  // the same for the whole group
+                if (tokens[q * NG] < 0) continue;  // the same for the whole group
                 if (a.c.format >= 0) {
                     const uint32_t code = ckpt::scale_code(in[q][v], a.c.format);
                     if (c < a.dvec) ckpt::store8(data[q], scales[q], a.c.format, c, in[q][v], code);
@@ -429,10 +473,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
                     f[j] = FULL ? fma2(mul2(add2(f[j], minus), rs), wf[j], bf[j])
                                 : mul2(mul2(f[j], rs), wf[j]);
                 if (POST) {
-                    const uint32_t row = row0 + q * a.slot;
                     F2 gf[4], xf[4];
-                    unpack8(a.streams == 3 ? ld_shared(row + a.in[2].off + 16 * c) : gate[v], gf);
-                    unpack8(ld_shared(row + a.in[1].off + 16 * c), xf);
+                    unpack8(a.streams == 3 ? ld_shared(at(2, q, c)) : gate[v], gf);
+                    unpack8(ld_shared(at(1, q, c)), xf);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) xf[j] = fma2(two(a.scale), mul2(gf[j], f[j]), xf[j]);
                     out[q][c] = pack8(xf);
@@ -471,8 +514,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
         const int64_t K_pad = ckpt::clamp_pad(K, a.pad_to, a.rows);
         if (K_pad > K) zero_tail<S>(a, K, K_pad);
     }
+    const Deal<S> deal(K);
     if (threadIdx.x >= S::kConsumers) {
-        produce<S>(a, sm, ring, K, !POST, a.kind != kNoNorm);
+        produce<S>(a, sm, ring, deal, !POST, a.kind != kNoNorm);
         return;
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
@@ -497,12 +541,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
         if constexpr (CODED) {
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                const int64_t r = row_of<S>(st, group * R + q);
+                const int64_t r = deal.row(st, q * NG + group);
+                const bool on = deal.has(st, q * NG + group);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int c = v * G + i;
                     code[q][v] =
-                        r < K && c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
+                        on && c < a.dvec ? __ldg(a.c.scales + r * a.c.ld_scales + (c >> 2)) : 127u;
                 }
             }
         }
@@ -510,15 +555,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     load_codes(0);
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t st = 0; row_of<S>(st, 0) < K; ++st) {
+    for (int64_t st = 0; deal.any(st); ++st) {
         if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
-        const uint32_t row0 = ring + (uint32_t)(s * S::kRows + group * R) * a.slot;
-        const int32_t* token = &sm->token[s][group * R];
-        const float2* stats = &sm->stats[s][group * R];  // (mean, rstd)
+        // row q of this group is row q NG + group of the stage
+        const int32_t* tokens = &sm->token[s][group];
+        const float2* stats = &sm->stats[s][group];  // (mean, rstd)
+        const uint32_t base0 = slot_addr<S>(a, ring, s, 0, group);
+        auto at = [&](int k, int q, int c) {  // vector c of stream k
+            return S::kNarrow ? slot_addr<S>(a, ring, s, k, q * NG + group) + 16 * c
+                              : base0 + a.in[k].off + q * (NG * a.slot) + 16 * c;
+        };
         uint4* out[R];
 #pragma unroll
         for (int q = 0; q < R; ++q)
-            out[q] = POST ? a.y + row_of<S>(st, group * R + q) * a.ld_y : a.x + (int64_t)token[q] * a.ld_x;
+            out[q] = POST ? a.y + deal.row(st, q * NG + group) * a.ld_y : a.x + (int64_t)tokens[q * NG] * a.ld_x;
         uint4 xin[POST ? 1 : R][V];
         if constexpr (!POST) {
 #pragma unroll
@@ -526,18 +576,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     const int c = v * G + i;
-                    if (token[q] >= 0 && c < a.dvec) xin[q][v] = out[q][c];
+                    if (tokens[q * NG] >= 0 && c < a.dvec) xin[q][v] = out[q][c];
                 }
         }
         auto vhat = [&](int q, int v, F2* f) {
             const int c = v * G + i;
-            const uint32_t row = row0 + q * a.slot;
-            const float2 m = stats[q];
+            const float2 m = stats[q * NG];
             if constexpr (CODED) {
                 // without a mean, rstd goes into the power-of-two scale: the same values
-                ckpt::decode8(ld_shared8(row + 8 * c), code[q][v], a.c.format, f, FULL ? 1.f : m.y);
+                ckpt::decode8(ld_shared8(at(0, q, 0) + 8 * c), code[q][v], a.c.format, f, FULL ? 1.f : m.y);
             } else {
-                unpack8(ld_shared(row + 16 * c), f);
+                unpack8(ld_shared(at(0, q, c)), f);
             }
             if (FULL) {
 #pragma unroll
@@ -550,10 +599,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
         // Gradient of the row's output (POST: dx).  The residual scale goes into rstd below and
         // into the column sums at the end, a gate of one row into the weights.
         auto grad = [&](int q, int v, F2* f) {
-            unpack8(ld_shared(row0 + q * a.slot + a.in[1].off + 16 * (v * G + i)), f);
+            unpack8(ld_shared(at(1, q, v * G + i)), f);
         };
         auto token_gate = [&](int q, int v, F2* f) {
-            unpack8(ld_shared(row0 + q * a.slot + a.in[2].off + 16 * (v * G + i)), f);
+            unpack8(ld_shared(at(2, q, v * G + i)), f);
         };
         // weights of vector v, times the gate of one row
         auto weight_gate = [&](int v, F2* f) {
@@ -576,7 +625,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             weight_gate(v, wf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                if (token[q] < 0) continue;  // no row: nothing goes into the sums
+                if (tokens[q * NG] < 0) continue;  // no row: nothing goes into the sums
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 grad(q, v, gg);
@@ -587,7 +636,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             bf[j] = mul2(mul2(gg[j], two(a.scale)), fma2(vv[j], wf[j], bf[j]));
-                        a.dgate_rows[row_of<S>(st, group * R + q) * a.ld_dgate + c] = pack8(bf);
+                        a.dgate_rows[deal.row(st, q * NG + group) * a.ld_dgate + c] = pack8(bf);
                     }
                     F2 gf[4];
                     token_gate(q, v, gf);
@@ -623,7 +672,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
             weight_gate(v, wf);
 #pragma unroll
             for (int q = 0; q < R; ++q) {
-                if (token[q] < 0) continue;
+                if (tokens[q * NG] < 0) continue;
                 F2 vv[4], gg[4];
                 vhat(q, v, vv);
                 grad(q, v, gg);
@@ -633,7 +682,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
 #pragma unroll
                     for (int j = 0; j < 4; ++j) gg[j] = mul2(gg[j], gf[j]);
                 }
-                const F2 rs = two(POST ? stats[q].y * a.scale : stats[q].y), c1 = two(p[q]), c2 = two(FULL ? p[P - R + q] : 0.f);
+                const F2 rs = two(POST ? stats[q * NG].y * a.scale : stats[q * NG].y), c1 = two(p[q]), c2 = two(FULL ? p[P - R + q] : 0.f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     gg[j] = fma2(vv[j], c1, mul2(gg[j], wf[j]));
