@@ -1719,13 +1719,14 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     a.n = n;
     a.d = d;
     a.tiles_m = (n + wg::TM - 1) / wg::TM;
+    a.tiles_n = (d + wg::TN - 1) / wg::TN;
     a.kept_total = kept_total;
     a.rows = rows;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         a.spin_limit_ns = (uint64_t)g_spin_ns;
     }
-    const int64_t tiles = (int64_t)a.tiles_m * ((d + wg::TN - 1) / wg::TN);
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (tiles > INT_MAX / 4) return LEMO_ERR_UNSUPPORTED;
     // More tiles than pairs: whole tiles, those of the last round in halves if they fit in it.
     const int64_t rest = tiles % pairs;

@@ -120,7 +120,7 @@ static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && STG_BYTES % 1024 == 
 struct Args {
     ckpt::View c;
     int n, d;
-    int tiles_m;
+    int tiles_m, tiles_n;
     int whole, items;            // items below `whole` are 256 x 256 tiles, the others 256 x 128 halves
     int splits;                  // pairs of a cluster; above 1 a cluster takes one item
     const int32_t* kept_total;
@@ -282,6 +282,11 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n) {
 // leave at least half of the pairs idle the host cuts its tiles in two
 // (4928 x 4096 x 4096 has 256 tiles for 74 pairs: 3.5 rounds instead of 4), and
 // a tile whose columns end within its first half is one anyway.
+// Tiles go in groups of GROUP row tiles, column by column: the group's dy stays in
+// L2 while the codes stream past it (8192 x 4096 x 11008: 654 MB read from DRAM,
+// 948 MB with all 16 row tiles in one group; 671 against 689 us).
+constexpr int GROUP = 8;
+
 struct Item {
     int n0, c0, width;  // width 0: nothing there
 };
@@ -295,8 +300,10 @@ __device__ __forceinline__ Item item_of(const Args& a, int i) {
         half = (i - a.whole) & 1;
         r.width = HALF;
     }
-    r.n0 = (t % a.tiles_m) * TM;
-    r.c0 = (t / a.tiles_m) * TN + half * HALF;
+    const int group = t / (GROUP * a.tiles_n), first = group * GROUP;
+    const int rows = min(GROUP, a.tiles_m - first), in = t - first * a.tiles_n;
+    r.n0 = (first + in % rows) * TM;
+    r.c0 = (in / rows) * TN + half * HALF;
     if (a.d - r.c0 <= HALF) r.width = HALF;
     if (r.c0 >= a.d) r.width = 0;
     return r;
