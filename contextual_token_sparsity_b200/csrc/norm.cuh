@@ -58,6 +58,7 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxRows = 32;    // rows of a stage: one per lane of the producer warp
 constexpr int kMaxWarps = 20;   // consumer warps
 constexpr int kMaxSmem = 220 * 1024;
+constexpr uint64_t kDrainNs = 2000000000ull;  // bound of the wait for copies in flight, at the end
 
 // G threads per group, V vectors per thread, R rows per group and stage.
 template <int G_, int V_, int R_>
@@ -116,6 +117,7 @@ struct Smem {
     int32_t token[kMaxStages][kMaxRows];  // -1: no row, or refused
     float2 stats[kMaxStages][kMaxRows];
     float red[2][kMaxWarps][8];           // per consumer warp, two alternating buffers
+    int32_t nothing[kMaxRows];            // -1: the tokens of a warp that gave up
     int abort_flag;
 };
 constexpr int kRing = 5120;  // offset of the ring
@@ -308,18 +310,18 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
             ph ^= 1;
         }
     }
-    if (!ok) {  // every copy in flight lands before the CTA leaves
-        for (int64_t j = st > a.stages ? st - a.stages : 0; j < st; ++j) {
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&sm->full[j % a.stages], (uint32_t)(j / a.stages) & 1) &&
-                   globaltimer_ns() - t0 < a.spin_limit_ns) {
-            }
+    // every copy in flight lands before the CTA leaves, also where its consumers gave up
+    for (int64_t j = st > a.stages ? st - a.stages : 0; j < st; ++j) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&sm->full[j % a.stages], (uint32_t)(j / a.stages) & 1) &&
+               globaltimer_ns() - t0 < kDrainNs) {
         }
     }
 }
 
 template <typename S>
 __device__ __forceinline__ void init_ring(const Args& a, Smem* sm) {
+    if (threadIdx.x < kMaxRows) sm->nothing[threadIdx.x] = -1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&sm->full[s], 1);
@@ -374,10 +376,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
     }
     int s = 0;
     uint32_t ph = 0;
+    // A warp whose wait ran out (reported) goes through the rest of its stages without rows: its
+    // group's barriers need it.
+    bool alive = true;
     for (int64_t st = 0; deal.any(st); ++st) {
-        if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
+        alive = alive && wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns);
         // row q of this group is row q NG + group of the stage
-        const int32_t* tokens = &sm->token[s][group];
+        const int32_t* tokens = alive ? &sm->token[s][group] : sm->nothing;
         const uint32_t base0 = slot_addr<S>(a, ring, s, 0, group);
         auto at = [&](int k, int q, int c) {  // vector c of stream k
             return S::kNarrow ? slot_addr<S>(a, ring, s, k, q * NG + group) + 16 * c
@@ -555,10 +560,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     load_codes(0);
     int s = 0;
     uint32_t ph = 0;
+    // A warp whose wait ran out (reported) goes through the rest of its stages without rows: its
+    // group's barriers need it.
+    bool alive = true;
     for (int64_t st = 0; deal.any(st); ++st) {
-        if (!wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns)) return;
+        alive = alive && wait_warp(&sm->full[s], ph, sm, a.spin_limit_ns);
         // row q of this group is row q NG + group of the stage
-        const int32_t* tokens = &sm->token[s][group];
+        const int32_t* tokens = alive ? &sm->token[s][group] : sm->nothing;
         const float2* stats = &sm->stats[s][group];  // (mean, rstd)
         const uint32_t base0 = slot_addr<S>(a, ring, s, 0, group);
         auto at = [&](int k, int q, int c) {  // vector c of stream k

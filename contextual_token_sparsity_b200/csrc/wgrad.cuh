@@ -97,6 +97,7 @@ constexpr int STEPS = ROWS_PER_WORKER / 4;  // a warp takes 4 rows at a time
 constexpr int BOX = 32;             // columns of an output box (32 rows, 128 bytes each)
 constexpr int STG_BYTES = 32 * BOX * 4;
 constexpr int TMEM_COLS = 512;
+constexpr uint64_t kDrainNs = 2000000000ull;  // bound of the waits for copies and MMAs in flight, at the end
 
 struct Smem {
     uint64_t a_full[STAGES];     // each CTA: its dy tile landed
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (uint32_t j = first; j < it; ++j) {
                     const uint64_t t0 = globaltimer_ns();
                     while (!mbar_try_wait(&sm->a_full[j % STAGES], (j / STAGES) & 1) &&
-                           globaltimer_ns() - t0 < lim) {
+                           globaltimer_ns() - t0 < kDrainNs) {
                     }
                 }
             }
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // bounded: every MMA the leader issued completes before TMEM is freed
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(&sm->done, 0)) {
-                if (globaltimer_ns() - t0 > lim) {
+                if (globaltimer_ns() - t0 > kDrainNs) {
                     raise_error(LEMO_ERR_TIMEOUT);
                     break;
                 }

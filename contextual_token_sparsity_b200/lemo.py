@@ -438,7 +438,7 @@ def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y
     yp, ld_y = fit.mat(y, "y", _BF16, d)
     _check(load().lemo_norm_gather(
         norm, xp, ld_x, x_rows, d, fit.vec(weight, "weight", _BF16, d),
-        fit.vec(bias, "bias", _BF16, d), eps, fit.vec(kept_idx, "kept_idx", _INT32, 0),
+        fit.vec(bias, "bias", _BF16, d), eps, fit.vec(kept_idx, "kept_idx", _INT32, 1),
         fit.total(kept_total), pad_to, yp, ld_y, rows, _stats(fit, stats, rows),
         fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
         "lemo_norm_gather")
@@ -462,7 +462,7 @@ def lemo_norm_gather_backward(norm, dy, weight, stats, kept_idx, kept_total, dx,
     wsp, ws_bytes = _workspace(fit, ws, dweight is not None or dbias is not None)
     _check(load().lemo_norm_gather_backward(
         norm, dyp, ld_dy, rows, d, fit.vec(weight, "weight", _BF16, d), _stats(fit, stats, rows),
-        fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total), xp, ld_x,
+        fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total), xp, ld_x,
         0 if x is None else x.shape[0], fit.ckpt(checkpoint, "checkpoint", d, rows), dxp, ld_dx,
         dx.shape[0], fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), wsp,
         ws_bytes, _stream(stream)),
@@ -483,7 +483,7 @@ def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept
     _check(load().lemo_norm_scatter(
         norm, xp, ld_x, x_rows, d, yp, ld_y, rows, fit.vec(weight, "weight", _BF16, d),
         fit.vec(bias, "bias", _BF16, d), eps, gp, ld_gate, scale,
-        fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total), _stats(fit, stats, rows),
+        fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total), _stats(fit, stats, rows),
         fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
         "lemo_norm_scatter")
 
@@ -511,7 +511,7 @@ def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_
     _check(load().lemo_norm_scatter_backward(
         norm, dxp, ld_dx, dx_rows, d, fit.vec(weight, "weight", _BF16, d),
         fit.vec(bias, "bias", _BF16, d), _stats(fit, stats, rows), gp, ld_gate, scale,
-        fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total), yp, ld_y,
+        fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total), yp, ld_y,
         fit.ckpt(checkpoint, "checkpoint", d, rows), pad_to, dyp, ld_dy, rows,
         fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), dg, dgr, ld_dgr,
         wsp, ws_bytes, _stream(stream)),
@@ -524,7 +524,7 @@ def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
     d = checkpoint.d
     xp, ld_x = fit.mat(x, "x", _BF16, d)
     _check(load().lemo_checkpoint_save(
-        xp, ld_x, x.shape[0], fit.vec(kept_idx, "kept_idx", _INT32, 0), fit.total(kept_total),
+        xp, ld_x, x.shape[0], fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total),
         fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream)),
         "lemo_checkpoint_save")
 

@@ -262,3 +262,35 @@ def test_offsets_past_32_bits():
     ok()
     a, b = f64(dy), f64(back)
     within(f64(dw), a.T @ b, 2 * (rows + 8) * U32 * (np.abs(a).T @ np.abs(b)), "dw")
+
+
+@pytest.mark.parametrize("d", [64, 1000, 4096, 8192])
+def test_a_wait_that_runs_out_is_reported(d):
+    """With a limit of a nanosecond some waits of the norm kernels' rings run out: their warps
+    go on without rows, the calls end, and the next ones are right."""
+    rng = np.random.default_rng(d)
+    K = 700
+    K_d = torch.tensor([K], dtype=torch.int32, device="cuda")
+    x, dy = bf16(draw(rng, K, d)), bf16(draw(rng, K, d))
+    c = lemo.make_checkpoint(torch.zeros(K, -(-d // 16) * 16, dtype=torch.uint8, device="cuda"),
+                             torch.zeros(K, -(-d // 128) * 4, dtype=torch.uint8, device="cuda"), 1, d)
+    ws = torch.empty(lemo.lemo_norm_workspace_size(d), dtype=torch.uint8, device="cuda")
+
+    def calls():
+        y, dx = torch.zeros_like(x), torch.zeros_like(x)
+        stats, dw = torch.zeros(K, 2, device="cuda"), torch.zeros(d, device="cuda")
+        lemo.lemo_norm_gather(LAYERNORM, x, None, None, EPS, None, K_d, 1, y, stats=stats, checkpoint=c)
+        lemo.lemo_norm_gather_backward(LAYERNORM, dy, None, stats, None, K_d, dx, ws, x=x, dweight=dw)
+        return y, stats, dx, dw
+
+    want = calls()
+    ok()
+    try:
+        lemo.lemo_set_test_hooks(-1, 1)
+        calls()
+        assert lemo.lemo_get_error() in (lemo.LEMO_OK, lemo.LEMO_ERR_TIMEOUT)
+    finally:
+        lemo.lemo_set_test_hooks(-1, 0)
+    got = calls()
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
