@@ -134,7 +134,8 @@ constexpr uint32_t kRareCode = 247;
 
 // Codes of 8 values under the group's scale byte.
 __device__ __forceinline__ uint2 encode8(uint4 v, uint32_t code, int format) {
-    const F2 inv = two(__uint_as_float((254u - code) << 23));  // 2^-k
+    // 2^-k; NaN for a group that is not finite (its codes become e4m3 NaN, or any int8)
+    const F2 inv = two(__uint_as_float(code == 255u ? 0x7fffffffu : (254u - code) << 23));
     F2 f[4];
     unpack8(v, f);
     if (code >= kRareCode) {
@@ -146,18 +147,14 @@ __device__ __forceinline__ uint2 encode8(uint4 v, uint32_t code, int format) {
             f[i] = f2(fminf(fmaxf(t.x, -most), most), fminf(fmaxf(t.y, -most), most));
         }
     }
-    uint2 q;
     if (format == kE4M3) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], inv);
-        q = make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = fma2(f[i], inv, two(kMagic));
-        q = make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
+        return make_uint2(e4m3x4(f[0], f[1]), e4m3x4(f[2], f[3]));
     }
-    const uint32_t none = format == kE4M3 ? 0x7f7f7f7fu : 0u;  // a group that is not finite
-    return make_uint2(code == 255u ? none : q.x, code == 255u ? none : q.y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = fma2(f[i], inv, two(kMagic));
+    return make_uint2(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]));
 }
 
 __device__ __forceinline__ void decode4(uint32_t q, F2 s, int format, F2* f) {

@@ -217,8 +217,8 @@ __device__ __forceinline__ uint4 ld_or(const uint4* p, int c, bool in, uint32_t 
 constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 
 // How K rows are dealt.  Narrow rows (up to 1024 values): a CTA takes `m`
-// neighbouring rows per stage (fewer than a stage holds when that is all there is
-// for every CTA), and a slot keeps the rows of a stream together, so that rows that
+// neighbouring rows per stage (as few as give every CTA the same number of stages),
+// and a slot keeps the rows of a stream together, so that rows that
 // are neighbours in memory come with one copy: 16384 x 512 is bound by the number
 // of copies, 18.4 us forward against 16.4.  Wide rows go round the CTAs one by one,
 // each with its streams together: at 8192 x 5120 43 us forward so, 45 as above.
@@ -227,8 +227,11 @@ struct Deal {
     int64_t K;
     int m;
     __device__ __forceinline__ explicit Deal(int64_t k) : K(k) {
-        const int64_t share = (k + gridDim.x - 1) / gridDim.x;
-        m = S::kNarrow && share < S::kRows ? (int)share : S::kRows;
+        m = S::kRows;
+        if (S::kNarrow && k > 0) {  // the same number of rows in each of a CTA's stages
+            const int64_t share = (k + gridDim.x - 1) / gridDim.x, stages = (share + m - 1) / m;
+            m = (int)((share + stages - 1) / stages);
+        }
     }
     __device__ __forceinline__ int64_t row(int64_t st, int j) const {
         return S::kNarrow ? (st * gridDim.x + blockIdx.x) * m + j

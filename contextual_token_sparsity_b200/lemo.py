@@ -142,12 +142,12 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object per call
         if raw is not None:
-            return raw(torch.cuda.current_device())
+            return raw(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -440,7 +440,7 @@ def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y
         norm, xp, ld_x, x_rows, d, fit.vec(weight, "weight", _BF16, d),
         fit.vec(bias, "bias", _BF16, d), eps, fit.vec(kept_idx, "kept_idx", _INT32, 1),
         fit.total(kept_total), pad_to, yp, ld_y, rows, _stats(fit, stats, rows),
-        fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
+        fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream, fit.dev)),
         "lemo_norm_gather")
 
 
@@ -465,7 +465,7 @@ def lemo_norm_gather_backward(norm, dy, weight, stats, kept_idx, kept_total, dx,
         fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total), xp, ld_x,
         0 if x is None else x.shape[0], fit.ckpt(checkpoint, "checkpoint", d, rows), dxp, ld_dx,
         dx.shape[0], fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), wsp,
-        ws_bytes, _stream(stream)),
+        ws_bytes, _stream(stream, fit.dev)),
         "lemo_norm_gather_backward")
 
 
@@ -484,7 +484,7 @@ def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept
         norm, xp, ld_x, x_rows, d, yp, ld_y, rows, fit.vec(weight, "weight", _BF16, d),
         fit.vec(bias, "bias", _BF16, d), eps, gp, ld_gate, scale,
         fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total), _stats(fit, stats, rows),
-        fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream)),
+        fit.ckpt(checkpoint, "checkpoint", d, rows), _stream(stream, fit.dev)),
         "lemo_norm_scatter")
 
 
@@ -514,7 +514,7 @@ def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_
         fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total), yp, ld_y,
         fit.ckpt(checkpoint, "checkpoint", d, rows), pad_to, dyp, ld_dy, rows,
         fit.vec(dweight, "dweight", _FP32, d), fit.vec(dbias, "dbias", _FP32, d), dg, dgr, ld_dgr,
-        wsp, ws_bytes, _stream(stream)),
+        wsp, ws_bytes, _stream(stream, fit.dev)),
         "lemo_norm_scatter_backward")
 
 
@@ -525,7 +525,7 @@ def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
     xp, ld_x = fit.mat(x, "x", _BF16, d)
     _check(load().lemo_checkpoint_save(
         xp, ld_x, x.shape[0], fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total),
-        fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream)),
+        fit.ckpt(checkpoint, "checkpoint", d, 0), _stream(stream, fit.dev)),
         "lemo_checkpoint_save")
 
 
@@ -536,7 +536,7 @@ def lemo_checkpoint_restore(checkpoint, kept_total, pad_to, y, stream=None):
     yp, ld_y = fit.mat(y, "y", _BF16, d)
     _check(load().lemo_checkpoint_restore(
         fit.ckpt(checkpoint, "checkpoint", d, rows), fit.total(kept_total), pad_to, yp, ld_y, rows,
-        _stream(stream)),
+        _stream(stream, fit.dev)),
         "lemo_checkpoint_restore")
 
 
@@ -552,7 +552,7 @@ def lemo_gated_mlp(gate, up, kept_total, pad_to, a, gate_checkpoint=None, up_che
     _check(load().lemo_gated_mlp(
         gp, ld_g, up_, ld_u, d, fit.total(kept_total), pad_to, ap, ld_a, rows,
         fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
-        fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), _stream(stream)),
+        fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), _stream(stream, fit.dev)),
         "lemo_gated_mlp")
 
 
@@ -568,7 +568,7 @@ def lemo_gated_mlp_backward(gate_checkpoint, up_checkpoint, da, kept_total, pad_
     _check(load().lemo_gated_mlp_backward(
         fit.ckpt(gate_checkpoint, "gate_checkpoint", d, rows),
         fit.ckpt(up_checkpoint, "up_checkpoint", d, rows), dap, ld_da, fit.total(kept_total),
-        pad_to, dgp, ld_dg, dup_, ld_du, ap, ld_a, rows, _stream(stream)),
+        pad_to, dgp, ld_dg, dup_, ld_du, ap, ld_a, rows, _stream(stream, fit.dev)),
         "lemo_gated_mlp_backward")
 
 
@@ -582,7 +582,7 @@ def lemo_checkpoint_weight_grad(checkpoint, dy, kept_total, dw, stream=None, n=N
     dwp, ld_dw = fit.mat(dw, "dw", _FP32, d, n, 4)
     _check(load().lemo_checkpoint_weight_grad(
         fit.ckpt(checkpoint, "checkpoint", d, rows), dyp, ld_dy, rows, n, fit.total(kept_total),
-        dwp, ld_dw, _stream(stream)),
+        dwp, ld_dw, _stream(stream, fit.dev)),
         "lemo_checkpoint_weight_grad")
 
 
