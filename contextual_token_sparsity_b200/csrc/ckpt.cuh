@@ -44,7 +44,8 @@ struct View {
     int64_t ld_scales;
 };
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+// (a product: it runs on the FMA pipe, the integer pipe being the busiest here)
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w * 65536u); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // Two fp32 values worked on by one instruction.
@@ -98,20 +99,6 @@ __device__ __forceinline__ uint4 pack8(const F2* f) {
     return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
 
-// Scale byte of the group of four lanes that this lane belongs to, from the
-// lane's 8 values (zeros where it has none).  Called by whole warps.
-// magnitude = 1.man 2^(exp - 127); 448 = (1 + 96/128) 2^8, 127 = (1 + 126/128) 2^6:
-// the byte is exp - 8 or exp - 6, one more where man is above 96 or 126.
-__device__ __forceinline__ uint32_t scale_code(uint4 v, int format) {
-    constexpr uint32_t kMag = 0x7fff7fffu;
-    uint32_t m = __vmaxu2(__vmaxu2(v.x & kMag, v.y & kMag), __vmaxu2(v.z & kMag, v.w & kMag));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int mag = (int)max(m & 0xffffu, m >> 16);
-    const int code = format == kE4M3 ? ((mag + 31) >> 7) - 8 : ((mag + 1) >> 7) - 6;
-    return mag >= 0x7f80 ? 255u : (uint32_t)max(code, kMinCode);
-}
-
 __device__ __forceinline__ uint32_t e4m3x4(F2 a, F2 b) {
     const float2 x = unf2(a), y = unf2(b);
     uint16_t lo, hi;
@@ -128,23 +115,40 @@ __device__ __forceinline__ uint32_t low_bytes(F2 a, F2 b) {
                        __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
 }
 
-// Scale bytes from here on are rare: the one of each format under which a
-// magnitude next to 2^128 could round up to 2^128 (247, 249), and 255.
-constexpr uint32_t kRareCode = 247;
+// Maximum of the magnitudes of two bf16 pairs (signs arbitrary), NaN if there is one.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
-// Codes of 8 values under the group's scale byte.
-__device__ __forceinline__ uint2 encode8(uint4 v, uint32_t code, int format) {
-    // 2^-k; NaN for a group that is not finite (its codes become e4m3 NaN, or any int8)
-    const F2 inv = two(__uint_as_float(code == 255u ? 0x7fffffffu : (254u - code) << 23));
+// Codes of this lane's 8 values (zeros where it has none) and the scale byte of
+// the group of four lanes that it belongs to.  Called by whole warps.
+// Largest magnitude = 1.man 2^(exp - 127); 448 = (1 + 96/128) 2^8 and
+// 127 = (1 + 126/128) 2^6: the byte is exp - 8 or exp - 6, one more where man is
+// above 96 or 126, i.e. where adding 31 or 1 carries.  u = 128 (byte + 8 or 6).
+__device__ __forceinline__ uint2 quantise8(uint4 v, int format, uint32_t& code) {
+    uint32_t m = max_abs2(max_abs2(v.x, v.y), max_abs2(v.z, v.w));
+    m = max_abs2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_abs2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int mag = (int)(max_abs2(m, __byte_perm(m, 0u, 0x1032)) & 0x7fffu);
+    const int bias = format == kE4M3 ? 8 : 6;
+    const uint32_t u = (uint32_t)max(mag + (format == kE4M3 ? 31 : 1), (kMinCode + bias) << 7) & 0xff80u;
+    code = (u >> 7) - bias;
+    F2 inv = two(__uint_as_float(((254u + bias) << 23) - u * 65536u));  // 2^-k
     F2 f[4];
     unpack8(v, f);
-    if (code >= kRareCode) {
-        const float most = (code != (format == kE4M3 ? 247u : 249u) ? 448.f : format == kE4M3 ? 240.f : 63.f) *
-                           __uint_as_float(code << 23);
+    if (u >= 0x7f80u) {  // not finite, or the one scale under which 2^128 is next to the largest value
+        if (mag >= 0x7f80) {
+            code = 255u;
+            inv = two(__uint_as_float(0x7fffffffu));  // the codes become e4m3 NaN, or any int8
+        } else {
+            const float most = (format == kE4M3 ? 240.f : 63.f) * __uint_as_float(code << 23);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 t = unf2(f[i]);
-            f[i] = f2(fminf(fmaxf(t.x, -most), most), fminf(fmaxf(t.y, -most), most));
+            for (int i = 0; i < 4; ++i) {
+                const float2 t = unf2(f[i]);
+                f[i] = f2(fminf(fmaxf(t.x, -most), most), fminf(fmaxf(t.y, -most), most));
+            }
         }
     }
     if (format == kE4M3) {
@@ -184,10 +188,14 @@ __device__ __forceinline__ void decode8(uint2 q, uint32_t code, int format, F2* 
     decode4(q.y, s, format, f + 2);
 }
 
-// Vector `vec` of a row: `data` and `scales` point at the row's first code and scale.
-__device__ __forceinline__ void store8(uint8_t* data, uint8_t* scales, int format, int vec, uint4 v,
-                                       uint32_t code) {
-    *reinterpret_cast<uint2*>(data + 8 * vec) = encode8(v, code, format);
+// Quantises vector `vec` of a row (`in`: the lane has one) whose codes and scales
+// start at `data` and `scales`.  Called by whole warps.
+__device__ __forceinline__ void save8(uint8_t* data, uint8_t* scales, int format, int vec, bool in,
+                                      uint4 v) {
+    uint32_t code;
+    const uint2 q = quantise8(v, format, code);
+    if (!in) return;
+    *reinterpret_cast<uint2*>(data + 8 * vec) = q;
     if ((vec & 3) == 0) scales[vec >> 2] = (uint8_t)code;
 }
 
@@ -239,23 +247,27 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const RowsArgs a) {
             if (lane == 0) raise_error(LEMO_ERR_INVALID_ARG);
             continue;
         }
-        const uint4* src = a.x + t * a.ld;
-        uint8_t* data = a.c.data + r * a.c.ld;
-        uint8_t* scales = a.c.scales + r * a.c.ld_scales;
-        for (int c0 = 0; c0 < a.dvec; c0 += 32 * kUnroll) {
+        // lane's pointers: its vectors are 32 apart
+        const uint4* src = a.x + t * a.ld + lane;
+        uint8_t* data = a.c.data + r * a.c.ld + 8 * lane;
+        uint8_t* scales = a.c.scales + r * a.c.ld_scales + (lane >> 2);
+        for (int left = a.dvec - lane; left + lane > 0; left -= 32 * kUnroll) {
             uint4 v[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int c = c0 + 32 * u + lane;
-                v[u] = c < a.dvec ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int u = 0; u < kUnroll; ++u)
+                v[u] = 32 * u < left ? __ldg(src + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int c = c0 + 32 * u + lane;
-                if (c0 + 32 * u >= a.dvec) break;  // warp-uniform
-                const uint32_t code = scale_code(v[u], a.c.format);
-                if (c < a.dvec) store8(data, scales, a.c.format, c, v[u], code);
+                if (32 * u >= left + lane) break;  // warp-uniform
+                uint32_t code;
+                const uint2 q = quantise8(v[u], a.c.format, code);
+                if (32 * u >= left) continue;
+                *reinterpret_cast<uint2*>(data + 256 * u) = q;
+                if ((lane & 3) == 0) scales[8 * u] = (uint8_t)code;
             }
+            src += 32 * kUnroll;
+            data += 256 * kUnroll;
+            scales += 8 * kUnroll;
         }
     }
 }
@@ -389,18 +401,12 @@ __global__ void __launch_bounds__(kThreads, 4) gated_kernel(const GatedArgs p) {
             if (r[k] >= K_pad) break;
             const bool in = c[k] < p.dvec;
             if (r[k] < K) {
-                if (p.cg.format >= 0) {
-                    const uint32_t code = scale_code(g[k], p.cg.format);
-                    if (in)
-                        store8(p.cg.data + r[k] * p.cg.ld, p.cg.scales + r[k] * p.cg.ld_scales, p.cg.format,
-                               c[k], g[k], code);
-                }
-                if (p.cu.format >= 0) {
-                    const uint32_t code = scale_code(u[k], p.cu.format);
-                    if (in)
-                        store8(p.cu.data + r[k] * p.cu.ld, p.cu.scales + r[k] * p.cu.ld_scales, p.cu.format,
-                               c[k], u[k], code);
-                }
+                if (p.cg.format >= 0)
+                    save8(p.cg.data + r[k] * p.cg.ld, p.cg.scales + r[k] * p.cg.ld_scales, p.cg.format, c[k],
+                          in, g[k]);
+                if (p.cu.format >= 0)
+                    save8(p.cu.data + r[k] * p.cu.ld, p.cu.scales + r[k] * p.cu.ld_scales, p.cu.format, c[k],
+                          in, u[k]);
             }
             F2 gf[4], uf[4];  // a row of the tail: zeros, SiLU(0) 0 = 0
             unpack8(g[k], gf);

@@ -468,10 +468,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 if (tokens[q * NG] < 0) continue;  // the same for the whole group
-                if (a.c.format >= 0) {
-                    const uint32_t code = ckpt::scale_code(in[q][v], a.c.format);
-                    if (c < a.dvec) ckpt::store8(data[q], scales[q], a.c.format, c, in[q][v], code);
-                }
+                if (a.c.format >= 0) ckpt::save8(data[q], scales[q], a.c.format, c, c < a.dvec, in[q][v]);
                 if (c >= a.dvec) continue;
                 F2 f[4];
                 unpack8(in[q][v], f);
