@@ -1611,7 +1611,8 @@ lemo_status lemo_checkpoint_restore(const lemo_checkpoint* checkpoint, const int
     a.rows = rows;
     a.pad_to = pad_to;
     a.c = view_of(checkpoint);
-    launch(lemo::ckpt::restore_kernel, ckpt_grid<lemo::ckpt::restore_kernel>(dev, sms, rows),
+    launch(lemo::ckpt::restore_kernel,
+           ckpt_grid<lemo::ckpt::restore_kernel>(dev, sms, rows * ((a.dvec + 31) / 32)),
            lemo::ckpt::kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
     return launch_status();
 }
