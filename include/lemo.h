@@ -563,7 +563,8 @@ typedef struct lemo_checkpoint {
  *             8-byte aligned; the backward pass needs it.
  * checkpoint  optional: x[t] is also saved there as row r (checkpoint->d = d,
  *             checkpoint->rows >= rows).
- * One pass over x.  Ids may repeat or come in any order.
+ * One pass over x.  Ids may repeat or come in any order.  The squares are summed
+ * in fp32: where that sum passes 3.4e38 the row's rstd is 0.
  */
 LEMO_API lemo_status lemo_norm_gather(lemo_norm norm, const uint16_t* x, int64_t ld_x,
                                       int64_t x_rows, int32_t d, const uint16_t* weight,

@@ -63,6 +63,13 @@ def test_save_restore_rows(K, fmt):
     check_save_restore(draw(rng, 701, 136), kept(rng, 701, K), fmt, pad_to=128)
 
 
+@pytest.mark.parametrize("L,K,d", [(10501, 10007, 40), (2400, 2300, 4104)])
+def test_save_restore_more_than_the_grid_holds(L, K, d):
+    """More rows, and more pieces of rows, than all warps take in one pass."""
+    rng = np.random.default_rng([L, d])
+    check_save_restore(draw(rng, L, d), kept(rng, L, K), "e4m3", extra=8, pad_to=128)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_every_magnitude_ties_and_nonfinite(fmt):
     """All bf16 exponents, both sides of the scale's switch, ties of the code
@@ -142,6 +149,10 @@ def test_gated_widths(d):
 @pytest.mark.parametrize("K", [0, 1, 128, 500])
 def test_gated_rows(K):
     check_gated(K, 520, "int8", "e4m3", pad_to=128)
+
+
+def test_gated_more_than_the_grid_holds():
+    check_gated(1500, 2056, "int8", "e4m3", extra=8, pad_to=128)
 
 
 def test_gated_saturated():
