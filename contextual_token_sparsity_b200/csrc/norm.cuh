@@ -30,7 +30,7 @@
 //
 // Measured on the copy rate's scale (6545 GB/s): gather of 8192 x 4096 RMS 27.6 us
 // (74 %), with an e4m3 checkpoint of the rows 35 us (73 %, issue slots 57 % busy), its
-// backward pass from bf16 rows 53 us (77 %) and from the checkpoint 57 us (63 %);
+// backward pass from bf16 rows 53 us (77 %) and from the checkpoint 53.6 us (67 %);
 // scatter of 16384 x 5120 RMS with a gate per token 103 us (99 %), its backward pass
 // 142 us (90 %).  Calls of less than 250 MB do not reach the copy rate: a plain copy
 // of 8192 x 4096 rows runs at 5.0 TB/s.
@@ -257,10 +257,12 @@ __device__ __forceinline__ uint32_t slot_addr(const Args& a, uint32_t ring, int 
 }
 
 // The producer warp: lane j brings row j of a stage; narrow rows that follow one
-// another in memory come with the first of them.
+// another in memory come with the first of them.  `coded`: the consumers read the
+// row's scale bytes from global memory right after the copies landed, so they are
+// asked for with them (8192 x 4096 backward from a checkpoint: 57.4 -> 53.6 us).
 template <typename S>
 __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, const Deal<S>& deal,
-                                        bool ascending, bool want_stats) {
+                                        bool ascending, bool want_stats, bool coded) {
     constexpr int NR = S::kRows;
     const int lane = threadIdx.x & 31;
     int s = 0;
@@ -302,6 +304,12 @@ __device__ __forceinline__ void produce(const Args& a, Smem* sm, uint32_t ring, 
         }
         __syncwarp();
         if (t >= 0) {
+            if (coded) {
+                const uint8_t* scales = a.c.scales + r * a.c.ld_scales;
+                const int last = (a.d - 1) / ckpt::kGroup;
+                for (int j = 0; j < last + 128; j += 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + min(j, last)));
+            }
             for (int i = 0; i < a.streams; ++i) {
                 const int64_t at = a.in[i].by_token ? t : r;
                 uint32_t bytes = a.in[i].bytes;
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) forward_kernel(const __grid_co
     }
     const Deal<S> deal(K);
     if (threadIdx.x >= S::kConsumers) {
-        produce<S>(a, sm, ring, deal, POST, false);
+        produce<S>(a, sm, ring, deal, POST, false, false);
         return;
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
@@ -528,7 +536,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) backward_kernel(const __grid_c
     }
     const Deal<S> deal(K);
     if (threadIdx.x >= S::kConsumers) {
-        produce<S>(a, sm, ring, deal, !POST, a.kind != kNoNorm);
+        produce<S>(a, sm, ring, deal, !POST, a.kind != kNoNorm, CODED);
         return;
     }
     const int group = threadIdx.x / G, i = threadIdx.x % G;
