@@ -337,8 +337,9 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const RowsArgs a) {
 // way; backward from the checkpoints with s = 1 / (1 + e^-g):
 //   dg = da u s (1 + g (1 - s)),  du = da g s,  a = g s u (recomputed).
 // Element-wise, bound by HBM: 8.06 bytes per value forward, 10.06 backward.  At
-// 8192 x 11008 with e4m3 checkpoints: forward 129 us (86 % of the rate of a copy,
-// the issue slots half busy), backward 150 us (92 %).
+// 8192 x 11008 with e4m3 checkpoints: forward 125 us (89 % of the rate of a copy,
+// issue slots next; 129 with a sigmoid from e^-|g| and a choice by g's sign),
+// backward 149 us (93 %).
 // ---------------------------------------------------------------------------
 struct GatedArgs {
     const uint4* g;
@@ -359,25 +360,24 @@ struct GatedArgs {
     View cg, cu;
 };
 
-// 1 / (1 + e^-g) of a pair, from t = e^-|g| <= 1 so that nothing overflows for
-// large -g.  t is the square of e^(-|g| / 2): the hardware exponential flushes
-// results below 2^-126 to 0, the square reaches the subnormals.  1 + t is in
-// [1, 2], where the hardware reciprocal needs no scaling.
+// s = 1 / (1 + e^-g) of a pair, as 2^-24 (1 / (2^-24 h^2 + 2^-24)) with
+// h = e^(-g / 2).  The hardware exponential and reciprocal flush results below 2^-126
+// to 0: the powers of two keep the quotient above that while s is above 2^-149, and
+// where h^2 overflows s is 0 anyway.  No choice by the sign of g is needed.
 __device__ __forceinline__ F2 sigmoid2(F2 g) {
-    constexpr float kHalfLog2e = 0.72134752f;
-    const float2 v = unf2(g);
-    float tx, ty, rx, ry;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(tx) : "f"(fabsf(v.x) * -kHalfLog2e));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ty) : "f"(fabsf(v.y) * -kHalfLog2e));
-    const F2 half = f2(tx, ty), t = mul2(half, half);
-    const float2 d = unf2(add2(t, two(1.f))), e = unf2(t);
+    const float2 z = unf2(mul2(g, two(-0.72134752f)));
+    float hx, hy, rx, ry;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(hx) : "f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(hy) : "f"(z.y));
+    const F2 h = f2(hx, hy);
+    const float2 d = unf2(fma2(mul2(h, two(0x1p-24f)), h, two(0x1p-24f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
-    return mul2(f2(v.x >= 0.f ? 1.f : e.x, v.y >= 0.f ? 1.f : e.y), f2(rx, ry));
+    return mul2(f2(rx, ry), two(0x1p-24f));
 }
 
 // A warp takes 32 vectors of a row at a time, with the loads of kPairs (backward
-// kBackPairs) such items in flight.  Forward 129 us with 2 and 141 with 1: the
+// kBackPairs) such items in flight.  Forward (before the present sigmoid) 129 us with 2 and 141 with 1: the
 // arithmetic of one covers the other's loads.  Backward 172 us with 2 and 150 with 1: it
 // has five streams, and twice the places in memory at a time cost the DRAM more than
 // the loads in flight bring (the same with three CTAs of more registers per SM instead
