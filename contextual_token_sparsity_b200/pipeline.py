@@ -14,6 +14,7 @@ them with the movement, and their backward passes:
     layer.gather_norm(...)     y = norm(x[kept]) w + b     (lemo_norm_gather)
     layer.scatter_norm(...)    x[kept] += s gate norm(y)   (lemo_norm_scatter)
     layer.checkpoint(...)      8-bit rows for one kept-row buffer (make_checkpoint)
+    layer.norm_stats()         row statistics of one forward call, for its backward call
 
 No step copies anything to the host; K stays on the device.
 """
@@ -59,6 +60,10 @@ class Layer:
         self.kept_total = torch.empty(1, dtype=torch.int32, device=device)
         self.y_rows = max(_round_up(self.total_L, pad_to), pad_to)
         self.y = torch.empty((self.y_rows, d), dtype=torch.bfloat16, device=device)
+        self.pre_stats, self.post_stats = self.norm_stats(), self.norm_stats()
+        # forward calls that wrote these since a backward call read them, and whether one has
+        self._forwards = {"pre_stats": 0, "post_stats": 0}
+        self._read = {"pre_stats": False, "post_stats": False}
 
     # -- the four steps ------------------------------------------------------
     def score(self, q, k, scale: float = 1.0, stream=None):
@@ -85,13 +90,38 @@ class Layer:
         self.scatter(x, y_out, stream)
 
     # -- norms around the sublayer, 8-bit checkpoints ---------------------------
+    # A forward call leaves the statistics (mean, rstd) of its rows in `stats`, and the backward
+    # call that follows it takes the same buffer.  Without `stats` both use the Layer's own
+    # (pre_stats for gather_norm, post_stats for scatter_norm), which hold one forward call:
+    # after a second one a backward call without `stats` is refused, since it could belong to
+    # either.  Two sublayers on one selection, micro-batches and forward calls that no backward
+    # call follows take a buffer each.
+    def norm_stats(self):
+        """An empty buffer for the statistics of one gather_norm or scatter_norm call."""
+        t = self.torch
+        return t.empty((self.y_rows, 2), dtype=t.float32, device=self.y.device)
+
     def _norm_buffers(self):
-        """Statistics of both norms and the backward passes' workspace (first use allocates)."""
+        """The backward passes' workspace (first use allocates)."""
         if not hasattr(self, "norm_ws"):
             t, dev = self.torch, self.y.device
-            self.pre_stats = t.empty((self.y_rows, 2), dtype=t.float32, device=dev)
-            self.post_stats = t.empty((self.y_rows, 2), dtype=t.float32, device=dev)
             self.norm_ws = t.empty(lemo.lemo_norm_workspace_size(self.d), dtype=t.uint8, device=dev)
+
+    def _own_stats(self, which: str, where: str):
+        """The Layer's own statistics, for a backward call."""
+        n = self._forwards[which]
+        if n != 1:
+            err = lemo.LemoError(lemo.LEMO_ERR_INVALID_ARG, where)
+            err.args = (f"{where}: {n} forward calls wrote the layer's own statistics; pass the same "
+                        "stats to a forward call and its backward call",)
+            raise err
+        return getattr(self, which)
+
+    def _wrote(self, which: str, own: bool):
+        """After a forward call: once read, the own statistics end with the next one."""
+        if self._read[which]:
+            self._forwards[which], self._read[which] = 0, False
+        self._forwards[which] += own
 
     def checkpoint(self, format: int, width: int | None = None):
         """An empty checkpoint for a kept-row buffer of `width` columns (d by default)."""
@@ -101,37 +131,51 @@ class Layer:
             t.empty((self.y_rows, _round_up(-(-d // 32), 4)), dtype=t.uint8, device=dev), format, d)
 
     def gather_norm(self, norm, x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None,
-                    stream=None):
+                    stream=None, stats=None):
         self._norm_buffers()
         lemo.lemo_norm_gather(norm, x, weight, bias, eps, self.kept_idx, self.kept_total,
-                              self.pad_to, self.y, stats=self.pre_stats, checkpoint=checkpoint,
-                              stream=stream)
+                              self.pad_to, self.y, stats=self.pre_stats if stats is None else stats,
+                              checkpoint=checkpoint, stream=stream)
+        self._wrote("pre_stats", stats is None)
         return self.y
 
     def gather_norm_backward(self, norm, dy, dx, weight=None, x=None, checkpoint=None, dweight=None,
-                             dbias=None, stream=None):
+                             dbias=None, stream=None, stats=None):
         """dx[kept] += d loss / d x[kept], in place, from the gradient dy of gather_norm's rows."""
-        lemo.lemo_norm_gather_backward(norm, dy, weight, self.pre_stats, self.kept_idx,
-                                       self.kept_total, dx, self.norm_ws, x=x,
-                                       checkpoint=checkpoint, dweight=dweight, dbias=dbias,
-                                       stream=stream)
+        own = stats is None
+        if own:
+            stats = self._own_stats("pre_stats", "gather_norm_backward")
+        self._norm_buffers()
+        lemo.lemo_norm_gather_backward(norm, dy, weight, stats, self.kept_idx, self.kept_total, dx,
+                                       self.norm_ws, x=x, checkpoint=checkpoint, dweight=dweight,
+                                       dbias=dbias, stream=stream)
+        if own:
+            self._read["pre_stats"] = True
 
     def scatter_norm(self, norm, x, y_out, weight=None, bias=None, eps: float = 1e-5, gate=None,
-                     scale: float = 1.0, checkpoint=None, stream=None):
+                     scale: float = 1.0, checkpoint=None, stream=None, stats=None):
         self._norm_buffers()
-        stats = None if norm == lemo.LEMO_NORM_NONE else self.post_stats
+        own = stats is None and norm != lemo.LEMO_NORM_NONE
         lemo.lemo_norm_scatter(norm, x, y_out, weight, bias, eps, gate, scale, self.kept_idx,
-                               self.kept_total, stats=stats, checkpoint=checkpoint, stream=stream)
+                               self.kept_total, stats=self.post_stats if own else stats,
+                               checkpoint=checkpoint, stream=stream)
+        if norm != lemo.LEMO_NORM_NONE:
+            self._wrote("post_stats", own)
 
     def scatter_norm_backward(self, norm, dx, dy_out, weight=None, bias=None, gate=None,
                               scale: float = 1.0, y_out=None, checkpoint=None, dweight=None,
-                              dbias=None, dgate=None, stream=None):
+                              dbias=None, dgate=None, stream=None, stats=None):
         """dy_out = the gradient of scatter_norm's y_out, zero-padded; dx is only read."""
-        stats = None if norm == lemo.LEMO_NORM_NONE else self.post_stats
+        own = stats is None and norm != lemo.LEMO_NORM_NONE
+        if own:
+            stats = self._own_stats("post_stats", "scatter_norm_backward")
+        self._norm_buffers()
         lemo.lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, self.kept_idx,
                                         self.kept_total, self.pad_to, dy_out, self.norm_ws,
                                         y=y_out, checkpoint=checkpoint, dweight=dweight,
                                         dbias=dbias, dgate=dgate, stream=stream)
+        if own:
+            self._read["post_stats"] = True
 
     # -- helpers for checking results ----------------------------------------
     def block_max_list(self):

@@ -1,0 +1,74 @@
+"""pipeline.Layer with norms on a GPU: sublayers that share one Layer."""
+
+import numpy as np
+import pytest
+import torch
+
+from contextual_token_sparsity_b200 import lemo
+from contextual_token_sparsity_b200.pipeline import Layer
+from sublayer_common import EPS, bf16, draw, ok
+
+pytestmark = pytest.mark.gpu
+RMS, LAYERNORM = lemo.LEMO_NORM_RMS, lemo.LEMO_NORM_LAYER
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda_ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    lemo.lemo_set_test_hooks(-1, 0)
+
+
+def _layer(lengths, d):
+    layer = Layer(lengths, 1, 64, 64, d)
+    layer.block_scores.copy_(torch.arange(layer.total_blocks, device="cuda") % 3)
+    layer.select(0.5)
+    ok()
+    assert 0 < int(layer.kept_total.item()) < layer.total_L
+    return layer
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_two_sublayers_on_one_layer(saved):
+    """Both forward passes before the first backward pass: every gradient is the one that a
+    Layer per sublayer gives, bit for bit."""
+    rng = np.random.default_rng([6, saved])
+    lengths, d = [300, 129], 264
+    L = sum(lengths)
+    one, apart = _layer(lengths, d), [_layer(lengths, d) for _ in range(2)]
+    rows = one.y_rows
+    x0 = [bf16(draw(rng, L, d, scale=s)) for s in (1.0, 5.0)]      # statistics that differ
+    o = [bf16(draw(rng, rows, d, scale=s, add=0.5)) for s in (0.2, 3.0)]
+    w = [bf16(draw(rng, d, add=1.0)) for _ in range(4)]
+    dy = [bf16(draw(rng, rows, d)) for _ in range(2)]
+    dx0 = bf16(draw(rng, L, d))
+    fmt = lemo.LEMO_CHECKPOINT_E4M3
+
+    def run(layers, stats):
+        grads, cks = [], []
+        x = [t.clone() for t in x0]
+        for i, layer in enumerate(layers):
+            cks.append([layer.checkpoint(fmt) if saved else None for _ in range(2)])
+            layer.gather_norm(RMS, x[i], w[i], None, EPS, checkpoint=cks[i][0], stats=stats[i][0])
+            layer.scatter_norm(LAYERNORM, x[i], o[i], w[2 + i], None, EPS, checkpoint=cks[i][1],
+                               stats=stats[i][1])
+        for i in (1, 0):
+            layer, dx = layers[i], dx0.clone()
+            do, dw = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, d, device="cuda")
+            layer.scatter_norm_backward(LAYERNORM, dx, do, w[2 + i], y_out=None if saved else o[i],
+                                        checkpoint=cks[i][1], dweight=dw[0], dbias=dw[1], stats=stats[i][1])
+            layer.gather_norm_backward(RMS, dy[i], dx, w[i], x=None if saved else x0[i],
+                                       checkpoint=cks[i][0], dweight=dw[2], stats=stats[i][0])
+            grads += [dx, do, dw]
+        ok()
+        return grads
+
+    want = run(apart, [(None, None)] * 2)
+    got = run([one, one], [[one.norm_stats() for _ in range(2)] for _ in range(2)])
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # with the other call's statistics they are not (what the shared buffer used to give)
+    wrong = run([one, one], [[s, t] for s, t in [(one.norm_stats(), one.norm_stats())]] * 2)
+    assert not any(torch.equal(a, b) for a, b in zip(want[3:], wrong[3:]))
