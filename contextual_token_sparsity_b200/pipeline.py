@@ -101,11 +101,17 @@ class Layer:
         t = self.torch
         return t.empty((self.y_rows, 2), dtype=t.float32, device=self.y.device)
 
-    def _norm_buffers(self):
-        """The backward passes' workspace (first use allocates)."""
-        if not hasattr(self, "norm_ws"):
-            t, dev = self.torch, self.y.device
-            self.norm_ws = t.empty(lemo.lemo_norm_workspace_size(self.d), dtype=t.uint8, device=dev)
+    def _norm_ws(self, sums: bool, stream):
+        """Workspace of one backward call, from the allocator's memory of the stream that the call
+        runs on (of the graph, where it is captured): calls that overlap do not share it."""
+        if not sums:
+            return None
+        t = self.torch
+        if isinstance(stream, int):
+            stream = (t.cuda.default_stream(self.y.device) if stream < 2 else
+                      t.cuda.ExternalStream(stream, self.y.device))
+        with t.cuda.stream(stream):
+            return t.empty(lemo.lemo_norm_workspace_size(self.d), dtype=t.uint8, device=self.y.device)
 
     def _own_stats(self, which: str, where: str):
         """The Layer's own statistics, for a backward call."""
@@ -132,7 +138,6 @@ class Layer:
 
     def gather_norm(self, norm, x, weight=None, bias=None, eps: float = 1e-5, checkpoint=None,
                     stream=None, stats=None):
-        self._norm_buffers()
         lemo.lemo_norm_gather(norm, x, weight, bias, eps, self.kept_idx, self.kept_total,
                               self.pad_to, self.y, stats=self.pre_stats if stats is None else stats,
                               checkpoint=checkpoint, stream=stream)
@@ -145,16 +150,15 @@ class Layer:
         own = stats is None
         if own:
             stats = self._own_stats("pre_stats", "gather_norm_backward")
-        self._norm_buffers()
+        ws = self._norm_ws(dweight is not None or dbias is not None, stream)
         lemo.lemo_norm_gather_backward(norm, dy, weight, stats, self.kept_idx, self.kept_total, dx,
-                                       self.norm_ws, x=x, checkpoint=checkpoint, dweight=dweight,
-                                       dbias=dbias, stream=stream)
+                                       ws, x=x, checkpoint=checkpoint, dweight=dweight, dbias=dbias,
+                                       stream=stream)
         if own:
             self._read["pre_stats"] = True
 
     def scatter_norm(self, norm, x, y_out, weight=None, bias=None, eps: float = 1e-5, gate=None,
                      scale: float = 1.0, checkpoint=None, stream=None, stats=None):
-        self._norm_buffers()
         own = stats is None and norm != lemo.LEMO_NORM_NONE
         lemo.lemo_norm_scatter(norm, x, y_out, weight, bias, eps, gate, scale, self.kept_idx,
                                self.kept_total, stats=self.post_stats if own else stats,
@@ -169,11 +173,11 @@ class Layer:
         own = stats is None and norm != lemo.LEMO_NORM_NONE
         if own:
             stats = self._own_stats("post_stats", "scatter_norm_backward")
-        self._norm_buffers()
+        ws = self._norm_ws(any(g is not None for g in (dweight, dbias, dgate)), stream)
         lemo.lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, self.kept_idx,
-                                        self.kept_total, self.pad_to, dy_out, self.norm_ws,
-                                        y=y_out, checkpoint=checkpoint, dweight=dweight,
-                                        dbias=dbias, dgate=dgate, stream=stream)
+                                        self.kept_total, self.pad_to, dy_out, ws, y=y_out,
+                                        checkpoint=checkpoint, dweight=dweight, dbias=dbias,
+                                        dgate=dgate, stream=stream)
         if own:
             self._read["post_stats"] = True
 

@@ -72,3 +72,59 @@ def test_two_sublayers_on_one_layer(saved):
     # with the other call's statistics they are not (what the shared buffer used to give)
     wrong = run([one, one], [[s, t] for s, t in [(one.norm_stats(), one.norm_stats())]] * 2)
     assert not any(torch.equal(a, b) for a, b in zip(want[3:], wrong[3:]))
+
+
+def test_backward_calls_on_two_streams(monkeypatch):
+    """Calls of one Layer on two streams, and in two graphs, run on workspaces of their own and
+    give what they give one after the other."""
+    rng = np.random.default_rng(7)
+    lengths, d = [1500, 700], 1024
+    L = sum(lengths)
+    layer = _layer(lengths, d)
+    x, w = bf16(draw(rng, L, d)), bf16(draw(rng, d, add=1.0))
+    dy = [bf16(draw(rng, layer.y_rows, d)) for _ in range(2)]
+    layer.gather_norm(RMS, x, w)
+    used, call = [], lemo.lemo_norm_gather_backward
+
+    def spy(*a, **kw):
+        used.append(a[7].data_ptr())
+        call(*a, **kw)
+
+    monkeypatch.setattr(lemo, "lemo_norm_gather_backward", spy)
+    dx = [torch.zeros(L, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dw = [torch.zeros(d, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+
+    def run(where):
+        for t in dx + dw:
+            t.zero_()
+        torch.cuda.synchronize()
+        used.clear()
+        where()
+        torch.cuda.synchronize()
+        ok()
+        return [t.clone() for t in dx + dw]
+
+    def back(i, stream=None):
+        layer.gather_norm_backward(RMS, dy[i], dx[i], w, x=x, dweight=dw[i], stream=stream)
+
+    want = run(lambda: [back(i) for i in range(2)])
+    for handles in (streams, [s.cuda_stream for s in streams]):
+        got = run(lambda: [back(i, handles[i]) for i in range(2)])
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert used[0] != used[1]
+    assert all(torch.equal(a, b) for a, b in zip(want, run(lambda: [back(i, 0) for i in range(2)])))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    used.clear()
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            back(i)
+    assert used[0] != used[1]
+
+    def replay():
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, run(replay)))

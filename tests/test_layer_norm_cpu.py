@@ -131,3 +131,19 @@ def test_a_refused_forward_call_writes_nothing(layer, calls, monkeypatch):
                     layer.gather_norm(RMS, x) if name.endswith("gather") else layer.scatter_norm(RMS, x, y)
     layer.scatter_norm_backward(RMS, x, y, y_out=y)
     layer.gather_norm_backward(RMS, y, x, x=x)
+
+
+def test_backward_calls_do_not_share_a_workspace(layer, calls):
+    """Each call has its own (calls on two streams may overlap); without column sums there is none."""
+    x, y, dw = torch.zeros(49, D, dtype=torch.bfloat16), _rows(layer), torch.zeros(D)
+    layer.gather_norm(RMS, x)
+    layer.scatter_norm(RMS, x, y)
+    for _ in range(2):
+        layer.scatter_norm_backward(RMS, x, y, y_out=y, dgate=dw)
+        layer.gather_norm_backward(RMS, y, x, x=x, dbias=dw)
+    ws = [a[7 if name.endswith("gather_backward") else 11] for name, _, a, _ in calls.seen[2:]]
+    assert len({t.data_ptr() for t in ws}) == 4
+    assert all(t.numel() == lemo.lemo_norm_workspace_size(D) for t in ws)
+    layer.scatter_norm_backward(RMS, x, y, y_out=y)
+    layer.gather_norm_backward(RMS, y, x, x=x)
+    assert calls.seen[-1][2][7] is None and calls.seen[-2][2][11] is None
