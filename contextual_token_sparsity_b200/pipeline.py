@@ -95,7 +95,8 @@ class Layer:
     # (pre_stats for gather_norm, post_stats for scatter_norm), which hold one forward call:
     # after a second one a backward call without `stats` is refused, since it could belong to
     # either.  Two sublayers on one selection, micro-batches and forward calls that no backward
-    # call follows take a buffer each.
+    # call follows take a buffer each.  Every row has the Layer's d values (of wider tensors the
+    # first d columns).
     def norm_stats(self):
         """An empty buffer for the statistics of one gather_norm or scatter_norm call."""
         t = self.torch
@@ -140,7 +141,7 @@ class Layer:
                     stream=None, stats=None):
         lemo.lemo_norm_gather(norm, x, weight, bias, eps, self.kept_idx, self.kept_total,
                               self.pad_to, self.y, stats=self.pre_stats if stats is None else stats,
-                              checkpoint=checkpoint, stream=stream)
+                              checkpoint=checkpoint, stream=stream, d=self.d)
         self._wrote("pre_stats", stats is None)
         return self.y
 
@@ -153,7 +154,7 @@ class Layer:
         ws = self._norm_ws(dweight is not None or dbias is not None, stream)
         lemo.lemo_norm_gather_backward(norm, dy, weight, stats, self.kept_idx, self.kept_total, dx,
                                        ws, x=x, checkpoint=checkpoint, dweight=dweight, dbias=dbias,
-                                       stream=stream)
+                                       stream=stream, d=self.d)
         if own:
             self._read["pre_stats"] = True
 
@@ -162,7 +163,7 @@ class Layer:
         own = stats is None and norm != lemo.LEMO_NORM_NONE
         lemo.lemo_norm_scatter(norm, x, y_out, weight, bias, eps, gate, scale, self.kept_idx,
                                self.kept_total, stats=self.post_stats if own else stats,
-                               checkpoint=checkpoint, stream=stream)
+                               checkpoint=checkpoint, stream=stream, d=self.d)
         if norm != lemo.LEMO_NORM_NONE:
             self._wrote("post_stats", own)
 
@@ -177,7 +178,7 @@ class Layer:
         lemo.lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, self.kept_idx,
                                         self.kept_total, self.pad_to, dy_out, ws, y=y_out,
                                         checkpoint=checkpoint, dweight=dweight, dbias=dbias,
-                                        dgate=dgate, stream=stream)
+                                        dgate=dgate, stream=stream, d=self.d)
         if own:
             self._read["post_stats"] = True
 

@@ -147,3 +147,30 @@ def test_backward_calls_do_not_share_a_workspace(layer, calls):
     layer.scatter_norm_backward(RMS, x, y, y_out=y)
     layer.gather_norm_backward(RMS, y, x, x=x)
     assert calls.seen[-1][2][7] is None and calls.seen[-2][2][11] is None
+
+
+def test_rows_of_another_width_are_refused(layer, monkeypatch):
+    """Every row has the Layer's width: narrower ones would leave the rest of y as it was; of wider
+    ones the first d columns are taken."""
+    monkeypatch.setattr(lemo, "_device", lambda: -1)      # CPU tensors pass the device check
+    x, y = torch.zeros(49, D, dtype=torch.bfloat16), _rows(layer)
+    for name, args in (("gather_norm", (RMS, x[:, :32])), ("scatter_norm", (RMS, x[:, :32], y)),
+                       ("scatter_norm", (RMS, x, y[:, :32])),
+                       ("scatter_norm_backward", (NONE, x[:, :32], y)),
+                       ("gather_norm_backward", (RMS, y[:, :32], x)),
+                       ("gather_norm_backward", (RMS, y, x[:, :32]))):
+        kw = {} if name in ("gather_norm", "scatter_norm") else {"stats": layer.norm_stats()}
+        if name == "gather_norm_backward":
+            kw["x"] = x
+        if name == "scatter_norm_backward":
+            kw["y_out"] = y
+        with pytest.raises(lemo.LemoError) as e:
+            getattr(layer, name)(*args, **kw)
+        assert e.value.status == lemo.LEMO_ERR_INVALID_ARG and "has shape" in str(e.value), name
+    seen = Calls(monkeypatch).seen
+    wide = torch.zeros(49, 2 * D, dtype=torch.bfloat16)
+    layer.gather_norm(RMS, wide)
+    layer.scatter_norm(RMS, wide, y)
+    layer.scatter_norm_backward(RMS, wide, y, y_out=y)
+    layer.gather_norm_backward(RMS, y, wide, x=wide)
+    assert [kw.get("d") for _, _, _, kw in seen] == [D] * 4
