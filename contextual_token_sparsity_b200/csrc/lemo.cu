@@ -36,6 +36,7 @@ int g_sms[kMaxDevices];              // 0 = not queried yet
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 int g_skip_publish_tile = -1;
 int g_predict_skip_cta = -1;
+int g_sublayer_withhold = 0;
 int64_t g_spin_ns = kDefaultSpinNs;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1726,6 +1727,7 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     {
         std::lock_guard<std::mutex> lk(g_mu);
         a.spin_limit_ns = (uint64_t)g_spin_ns;
+        a.withhold = g_sublayer_withhold;
     }
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (tiles > INT_MAX / 4) return LEMO_ERR_UNSUPPORTED;
@@ -1781,6 +1783,11 @@ lemo_status lemo_get_error(lemo_stream stream) {
 void lemo_set_predict_test_hook(int32_t skip_cta) {
     std::lock_guard<std::mutex> lk(g_mu);
     g_predict_skip_cta = skip_cta < 0 ? -1 : skip_cta;
+}
+
+void lemo_set_sublayer_test_hook(int32_t withhold) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_sublayer_withhold = withhold != 0;
 }
 
 void lemo_set_test_hooks(int32_t select_skip_publish_tile, int64_t spin_limit_ns) {

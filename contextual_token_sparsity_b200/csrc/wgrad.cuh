@@ -130,6 +130,7 @@ struct Args {
     const int32_t* kept_total;
     int64_t rows;
     uint64_t spin_limit_ns;
+    int withhold;                // test hook: the first cluster's first stage never becomes ready
 };
 
 __device__ __forceinline__ void abort_pair(Smem* sm) {
@@ -341,7 +342,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm->a_full[s], 1);
-            mbar_init(&sm->ready[s], 2 * (TEAM + 1));
+            // (test hook: an arrival more than there will be)
+            mbar_init(&sm->ready[s], 2 * (TEAM + 1) + (a.withhold && cluster == 0 && s == 0 ? 1 : 0));
             mbar_init(&sm->used[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -388,13 +390,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (!ok) {  // every load in flight lands before the CTA leaves
-                const uint32_t first = it > STAGES ? it - STAGES : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    const uint64_t t0 = globaltimer_ns();
-                    while (!mbar_try_wait(&sm->a_full[j % STAGES], (j / STAGES) & 1) &&
-                           globaltimer_ns() - t0 < kDrainNs) {
-                    }
+            // every load in flight lands before the CTA leaves, also where another warp gave up
+            for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(&sm->a_full[j % STAGES], (j / STAGES) & 1) &&
+                       globaltimer_ns() - t0 < kDrainNs) {
                 }
             }
         }

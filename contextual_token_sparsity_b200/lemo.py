@@ -113,6 +113,7 @@ _SIGS = {
     "lemo_get_error": (ctypes.c_int, [_P]),
     "lemo_set_test_hooks": (None, [_I32, _I64]),
     "lemo_set_predict_test_hook": (None, [_I32]),
+    "lemo_set_sublayer_test_hook": (None, [_I32]),
 }
 
 _lib = None
@@ -597,3 +598,7 @@ def lemo_set_test_hooks(select_skip_publish_tile: int = -1, spin_limit_ns: int =
 
 def lemo_set_predict_test_hook(skip_cta: int = -1):
     load().lemo_set_predict_test_hook(int(skip_cta))
+
+
+def lemo_set_sublayer_test_hook(withhold: bool = False):
+    load().lemo_set_sublayer_test_hook(int(withhold))
