@@ -1261,6 +1261,7 @@ lemo_status run_norm_as(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     {
         std::lock_guard<std::mutex> lk(g_mu);
         a.spin_limit_ns = (uint64_t)g_spin_ns;
+        a.withhold = g_sublayer_withhold;
     }
     bool ok;
     if (a.dvec <= 32) ok = launch_norm<BWD, POST, FULL, CODED, Shape<32, 1, 2>>(a, dev, sms, st, grid);

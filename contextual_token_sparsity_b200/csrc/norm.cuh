@@ -116,6 +116,7 @@ struct Args {
     } in[3];
     uint32_t slot;            // bytes of one row's slot
     uint64_t spin_limit_ns;
+    int withhold;         // test hook: the first CTA's first slot never becomes free again
 };
 
 struct Smem {
@@ -343,7 +344,8 @@ __device__ __forceinline__ void init_ring(const Args& a, Smem* sm) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&sm->full[s], 1);
-            mbar_init(&sm->empty[s], S::kConsumers / 32);
+            // (test hook: an arrival more than there will be)
+            mbar_init(&sm->empty[s], S::kConsumers / 32 + (a.withhold && blockIdx.x == 0 && s == 0 ? 1 : 0));
         }
         sm->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

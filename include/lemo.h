@@ -743,10 +743,11 @@ LEMO_API void lemo_set_test_hooks(int32_t select_skip_publish_tile, int64_t spin
 LEMO_API void lemo_set_predict_test_hook(int32_t skip_cta);
 
 /*
- * Test hook of lemo_checkpoint_weight_grad (process-wide, not thread-safe):
- * with withhold != 0 one arrival of the first cluster's first stage does not
- * come, so that cluster's bounded waits run out and the call reports
- * LEMO_ERR_TIMEOUT; 0 disables it.
+ * Test hook of the norm calls and lemo_checkpoint_weight_grad (process-wide,
+ * not thread-safe): with withhold != 0 one arrival of the first cluster's (a
+ * norm's first CTA's) first stage does not come, so that its bounded waits run
+ * out and the call reports LEMO_ERR_TIMEOUT (a norm call with fewer rows than
+ * fill the first CTA's ring never waits for that stage); 0 disables it.
  */
 LEMO_API void lemo_set_sublayer_test_hook(int32_t withhold);
 

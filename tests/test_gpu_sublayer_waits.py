@@ -61,3 +61,54 @@ def test_weight_grad(K, rows, n, d, fmt):
     again = call()
     ok()
     assert torch.equal(want, again)
+
+
+# enough rows that every CTA uses its first slot again: at most 8 slots of 32 (d <= 256), 16
+# (512 and below), 8 (1024), 4, 2 or 1 rows on each of up to 296 CTAs
+@pytest.mark.parametrize("d,K", [(64, 80000), (512, 40000), (1000, 20000), (2048, 11000), (4096, 6000),
+                                 (5120, 5000), (8192, 5000), (16384, 2600)])
+def test_norms(d, K):
+    """The first CTA goes on without rows: its later rows are left as they were, everything else is
+    the same."""
+    rng = np.random.default_rng(d)
+    norm = lemo.LEMO_NORM_LAYER
+    g = torch.Generator("cuda").manual_seed(d)
+    x, dy = (torch.randn(K, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w, K_d = bf16(draw(rng, d, add=1.0)), dev_i32(K)
+    ck, data, scales = make_ckpt(K, d, "int8")
+    stats = torch.zeros(K, 2, device="cuda")
+    ws = torch.empty(lemo.lemo_norm_workspace_size(d), dtype=torch.uint8, device="cuda")
+
+    def gather():
+        y, st = torch.zeros_like(x), torch.zeros_like(stats)
+        lemo.lemo_norm_gather(norm, x, w, None, 1e-5, None, K_d, 1, y, stats=st)
+        return y, st
+
+    def scatter():
+        z = torch.zeros_like(x)
+        lemo.lemo_norm_scatter(norm, z, x, w, None, 1e-5, None, 1.0, None, K_d)
+        return (z,)
+
+    def gather_backward(saved=False):
+        dx, dw = torch.zeros_like(x), torch.zeros(d, device="cuda")
+        lemo.lemo_norm_gather_backward(norm, dy, w, stats, None, K_d, dx, ws, x=None if saved else x,
+                                       checkpoint=ck if saved else None, dweight=dw)
+        return dx, dw
+
+    def scatter_backward():
+        dv, dg = torch.zeros_like(x), torch.zeros(d, device="cuda")
+        lemo.lemo_norm_scatter_backward(norm, dy, w, None, stats, w, 0.5, None, K_d, 1, dv, ws, y=x, dgate=dg)
+        return dv, dg
+
+    lemo.lemo_norm_gather(norm, x, w, None, 1e-5, None, K_d, 1, torch.empty_like(x), stats=stats, checkpoint=ck)
+    for call in (gather, scatter, gather_backward, lambda: gather_backward(True), scatter_backward):
+        want = call()
+        ok()
+        got = withheld(call)
+        missing = (got[0] != want[0]).any(1)
+        assert missing.any() and (got[0][missing] == 0).all()
+        # the first CTA's share at most: one CTA of an SM each, at least 100 of them
+        assert int(missing.sum()) <= K // 100
+        again = call()
+        ok()
+        assert all(torch.equal(a, b) for a, b in zip(want, again))
