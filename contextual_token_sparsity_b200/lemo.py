@@ -383,13 +383,18 @@ def _device() -> int:
 
 class Checkpoint:
     """Rows in 8 bits: ``data`` uint8 [rows, >= d] (row stride a multiple of 16
-    bytes), ``scales`` uint8 [rows, >= ceil(d / 32)] (a multiple of 4)."""
+    bytes), ``scales`` uint8 [rows, >= ceil(d / 32)] (a multiple of 4).  Codes
+    are read 16 bytes at a time, so the memory behind the last row's codes has
+    to reach the next multiple of 16."""
 
     def __init__(self, data, scales, format: int, d: int):
         fit = _Fit("make_checkpoint")
         dp, ld_data = fit.mat(data, "data", _UINT8, d, 0, 16)
         sp, ld_scales = fit.mat(scales, "scales", _UINT8, -(-d // 32), data.shape[0], 4)
         self.data, self.scales, self.d, self.rows = data, scales, int(d), data.shape[0]
+        end = data.storage_offset() + (self.rows - 1) * ld_data + -(-self.d // 16) * 16
+        if self.rows and end > data.untyped_storage().nbytes():
+            fit.bad("data", "ends before the last row's codes reach a multiple of 16 bytes")
         self.device = data.get_device()
         self.struct = lemo_checkpoint(int(format), int(d), dp, ld_data, sp, ld_scales, self.rows)
         self.ref = ctypes.addressof(self.struct)

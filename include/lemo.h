@@ -539,7 +539,8 @@ typedef enum lemo_checkpoint_format {
 typedef struct lemo_checkpoint {
     int32_t format;      /* lemo_checkpoint_format                                    */
     int32_t d;           /* values per row, d % 8 == 0                                */
-    uint8_t* data;       /* DEVICE [rows, ld_data] codes, 16-byte aligned             */
+    uint8_t* data;       /* DEVICE [rows, ld_data] codes, 16-byte aligned; the bytes  */
+                         /* behind a row's codes up to a multiple of 16 are read      */
     int64_t ld_data;     /* bytes, multiple of 16, >= d                               */
     uint8_t* scales;     /* DEVICE [rows, ld_scales] scale bytes, 4-byte aligned      */
     int64_t ld_scales;   /* bytes, multiple of 4, >= ceil(d / 32)                     */
