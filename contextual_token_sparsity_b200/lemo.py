@@ -301,7 +301,9 @@ def lemo_segment_loss(h, w, targets, seg_rows, loss, ws, token_loss=None, dh=Non
 # the current CUDA device and has the type, row layout and sizes the call
 # needs; a tensor that does not fit raises LemoError(LEMO_ERR_INVALID_ARG).
 # ---------------------------------------------------------------------------
-_torch = _BF16 = _FP32 = _INT32 = _UINT8 = None  # torch and its dtypes, set with the first _Fit
+_torch = _Tensor = _BF16 = _FP32 = _INT32 = _UINT8 = None  # torch and its types, set with the first _Fit
+
+_NO_SHAPE = (AttributeError, ValueError, IndexError, TypeError)  # of unpacking the shape of something else
 
 
 class _Fit:
@@ -323,26 +325,39 @@ class _Fit:
     def mat(self, t, name, dtype, cols, rows=0, unit=8):
         """(pointer, row stride) of a 2-D tensor with contiguous rows; a single
         row's own stride says nothing, so its width rounded up to `unit` stands in."""
-        if t is not None:
+        try:
             shape = t.shape
             if len(shape) == 2 and t.dtype is dtype and t.get_device() == self.dev:
                 n, width = shape
                 ld, step = t.stride()
                 if n >= rows and width >= cols and (step == 1 or width == 1):
                     return t.data_ptr(), ld if n > 1 else -(-width // unit) * unit
+        except AttributeError:  # not a tensor
+            pass
         self.explain(t, name, dtype, (rows, cols))
 
     def vec(self, t, name, dtype, n):
         if t is None:
             return None
-        if (t.dtype is dtype and t.dim() == 1 and t.numel() >= n and t.is_contiguous()
-                and t.get_device() == self.dev):
-            return t.data_ptr()
+        try:
+            if (t.dtype is dtype and t.dim() == 1 and t.numel() >= n and t.is_contiguous()
+                    and t.get_device() == self.dev):
+                return t.data_ptr()
+        except AttributeError:  # not a tensor
+            pass
         self.explain(t, name, dtype, (n,))
+
+    def shapeless(self, **tensors):
+        """Explains which of the tensors that `mat` is going to check has no rows and columns."""
+        for name, t in tensors.items():
+            if not isinstance(t, _Tensor) or t.dim() != 2:
+                self.explain(t, name, _BF16, (0, 0))
 
     def explain(self, t, name, dtype, need):
         if t is None:
             self.bad(name, "is missing")
+        if not isinstance(t, _Tensor):
+            self.bad(name, "is not a tensor")
         if t.dtype is not dtype or t.dim() != len(need):
             self.bad(name, f"is not a {len(need)}-D {dtype} tensor")
         if t.get_device() != self.dev:
@@ -355,6 +370,12 @@ class _Fit:
         if kept_total is None:
             self.bad("kept_total", "is missing")
         return self.vec(kept_total, "kept_total", _INT32, 1)
+
+    def width(self, c, name):
+        """d of a checkpoint that has to be there."""
+        if not isinstance(c, Checkpoint):
+            self.bad(name, "is missing" if c is None else "is not a Checkpoint")
+        return c.d
 
     def ckpt(self, c, name, d, rows):
         if c is None:
@@ -369,9 +390,9 @@ class _Fit:
 
 
 def _bind_torch():
-    global _torch, _BF16, _FP32, _INT32, _UINT8
+    global _torch, _Tensor, _BF16, _FP32, _INT32, _UINT8
     import torch
-    _torch = torch
+    _torch, _Tensor = torch, torch.Tensor
     _BF16, _FP32, _INT32, _UINT8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
@@ -419,7 +440,7 @@ def _workspace(fit, ws, needed):
         if needed:
             fit.bad("ws", "is missing")
         return None, 0
-    if ws.get_device() != fit.dev or not ws.is_contiguous():
+    if not isinstance(ws, _Tensor) or ws.get_device() != fit.dev or not ws.is_contiguous():
         fit.bad("ws", "is not a contiguous tensor on the current CUDA device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -427,7 +448,7 @@ def _workspace(fit, ws, needed):
 def _gate(fit, gate, d, rows):
     if gate is None:
         return None, 0
-    if gate.dim() == 1:
+    if isinstance(gate, _Tensor) and gate.dim() == 1:
         return fit.vec(gate, "gate", _BF16, d), 0
     return fit.mat(gate, "gate", _BF16, d, rows)
 
@@ -437,9 +458,11 @@ def lemo_norm_gather(norm, x, weight, bias, eps, kept_idx, kept_total, pad_to, y
     """x bf16 [x_rows, >= d], y bf16 [rows, >= d], weight / bias bf16 [d] or
     None, stats fp32 [rows, 2] contiguous, kept_idx int32 (at least K) or None."""
     fit = _Fit("lemo_norm_gather")
-    x_rows, width = x.shape
+    try:
+        (x_rows, width), rows = x.shape, y.shape[0]
+    except _NO_SHAPE:
+        fit.shapeless(x=x, y=y)
     d = width if d is None else int(d)
-    rows = y.shape[0]
     xp, ld_x = fit.mat(x, "x", _BF16, d)
     yp, ld_y = fit.mat(y, "y", _BF16, d)
     _check(load().lemo_norm_gather(
@@ -460,7 +483,10 @@ def lemo_norm_gather_backward(norm, dy, weight, stats, kept_idx, kept_total, dx,
     one of x (the forward call's input) and checkpoint; dweight / dbias fp32
     [d] optional (accumulated); ws may be None without them."""
     fit = _Fit("lemo_norm_gather_backward")
-    rows, width = dy.shape
+    try:
+        rows, width = dy.shape
+    except _NO_SHAPE:
+        fit.shapeless(dy=dy)
     d = width if d is None else int(d)
     dyp, ld_dy = fit.mat(dy, "dy", _BF16, d)
     dxp, ld_dx = fit.mat(dx, "dx", _BF16, d)
@@ -480,9 +506,11 @@ def lemo_norm_scatter(norm, x, y, weight, bias, eps, gate, scale, kept_idx, kept
     """x bf16 [tokens, >= d] (updated in place), y bf16 [rows, >= d]; gate None,
     bf16 [d] (all tokens) or bf16 [rows, >= d] (per kept row)."""
     fit = _Fit("lemo_norm_scatter")
-    x_rows, width = x.shape
+    try:
+        (x_rows, width), rows = x.shape, y.shape[0]
+    except _NO_SHAPE:
+        fit.shapeless(x=x, y=y)
     d = width if d is None else int(d)
-    rows = y.shape[0]
     xp, ld_x = fit.mat(x, "x", _BF16, d)
     yp, ld_y = fit.mat(y, "y", _BF16, d)
     gp, ld_gate = _gate(fit, gate, d, rows)
@@ -501,15 +529,17 @@ def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_
     of y and checkpoint; dgate fp32 [d] (accumulated) for a gate of one row,
     bf16 [rows, >= d] (written) for a gate row per kept row."""
     fit = _Fit("lemo_norm_scatter_backward")
-    dx_rows, width = dx.shape
+    try:
+        (dx_rows, width), rows = dx.shape, dy.shape[0]
+    except _NO_SHAPE:
+        fit.shapeless(dx=dx, dy=dy)
     d = width if d is None else int(d)
-    rows = dy.shape[0]
     dxp, ld_dx = fit.mat(dx, "dx", _BF16, d)
     dyp, ld_dy = fit.mat(dy, "dy", _BF16, d)
     yp, ld_y = (None, 0) if y is None else fit.mat(y, "y", _BF16, d, rows)
     gp, ld_gate = _gate(fit, gate, d, rows)
     dg, dgr, ld_dgr = None, None, 0
-    if dgate is not None and dgate.dim() == 2:
+    if isinstance(dgate, _Tensor) and dgate.dim() == 2:
         dgr, ld_dgr = fit.mat(dgate, "dgate", _BF16, d, rows)
     else:
         dg = fit.vec(dgate, "dgate", _FP32, d)
@@ -527,7 +557,7 @@ def lemo_norm_scatter_backward(norm, dx, weight, bias, stats, gate, scale, kept_
 def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
     """x bf16 [tokens, >= checkpoint.d]; kept_idx int32 or None (row r is token r)."""
     fit = _Fit("lemo_checkpoint_save")
-    d = checkpoint.d
+    d = fit.width(checkpoint, "checkpoint")
     xp, ld_x = fit.mat(x, "x", _BF16, d)
     _check(load().lemo_checkpoint_save(
         xp, ld_x, x.shape[0], fit.vec(kept_idx, "kept_idx", _INT32, 1), fit.total(kept_total),
@@ -538,7 +568,11 @@ def lemo_checkpoint_save(x, kept_idx, kept_total, checkpoint, stream=None):
 def lemo_checkpoint_restore(checkpoint, kept_total, pad_to, y, stream=None):
     """y bf16 [rows, >= checkpoint.d], rows <= checkpoint.rows."""
     fit = _Fit("lemo_checkpoint_restore")
-    d, rows = checkpoint.d, y.shape[0]
+    d = fit.width(checkpoint, "checkpoint")
+    try:
+        rows = y.shape[0]
+    except _NO_SHAPE:
+        fit.shapeless(y=y)
     yp, ld_y = fit.mat(y, "y", _BF16, d)
     _check(load().lemo_checkpoint_restore(
         fit.ckpt(checkpoint, "checkpoint", d, rows), fit.total(kept_total), pad_to, yp, ld_y, rows,
@@ -550,7 +584,10 @@ def lemo_gated_mlp(gate, up, kept_total, pad_to, a, gate_checkpoint=None, up_che
                    stream=None, d=None):
     """gate, up, a bf16 [rows, >= d]; a = SiLU(gate) up."""
     fit = _Fit("lemo_gated_mlp")
-    rows, width = a.shape
+    try:
+        rows, width = a.shape
+    except _NO_SHAPE:
+        fit.shapeless(a=a)
     d = width if d is None else int(d)
     gp, ld_g = fit.mat(gate, "gate", _BF16, d, rows)
     up_, ld_u = fit.mat(up, "up", _BF16, d, rows)
@@ -566,7 +603,12 @@ def lemo_gated_mlp_backward(gate_checkpoint, up_checkpoint, da, kept_total, pad_
                             a=None, stream=None):
     """da, dgate, dup and the optional recomputed activation a: bf16 [rows, >= d]."""
     fit = _Fit("lemo_gated_mlp_backward")
-    d, rows = gate_checkpoint.d, dgate.shape[0]
+    d = fit.width(gate_checkpoint, "gate_checkpoint")
+    fit.width(up_checkpoint, "up_checkpoint")
+    try:
+        rows = dgate.shape[0]
+    except _NO_SHAPE:
+        fit.shapeless(dgate=dgate)
     dap, ld_da = fit.mat(da, "da", _BF16, d, rows)
     dgp, ld_dg = fit.mat(dgate, "dgate", _BF16, d)
     dup_, ld_du = fit.mat(dup, "dup", _BF16, d, rows)
@@ -581,8 +623,11 @@ def lemo_gated_mlp_backward(gate_checkpoint, up_checkpoint, da, kept_total, pad_
 def lemo_checkpoint_weight_grad(checkpoint, dy, kept_total, dw, stream=None, n=None):
     """dw fp32 [n, >= d] += dy^T xhat; dy bf16 [rows, >= n], n = dy's width."""
     fit = _Fit("lemo_checkpoint_weight_grad")
-    d = checkpoint.d
-    rows, width = dy.shape
+    d = fit.width(checkpoint, "checkpoint")
+    try:
+        rows, width = dy.shape
+    except _NO_SHAPE:
+        fit.shapeless(dy=dy)
     n = width if n is None else int(n)
     dyp, ld_dy = fit.mat(dy, "dy", _BF16, n)
     dwp, ld_dw = fit.mat(dw, "dw", _FP32, d, n, 4)
