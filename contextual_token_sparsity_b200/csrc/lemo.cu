@@ -1704,13 +1704,13 @@ lemo_status lemo_checkpoint_weight_grad(const lemo_checkpoint* checkpoint, const
     if (n % 8 != 0 || rows > (1 << 30)) return LEMO_ERR_UNSUPPORTED;
     if (!mat_ok(dy, ld_dy, n) || !dw || !aligned(dw, 16) || ld_dw < d || ld_dw % 4 != 0)
         return LEMO_ERR_INVALID_ARG;
-    if (rows == 0) return LEMO_OK;
     namespace wg = lemo::wgrad;
     int dev = 0;
     const int sms = device_sms(&dev);
     if (sms <= 0) return LEMO_ERR_CUDA;
     CUtensorMap tm_dy, tm_dw;
-    if (!encode_operand(&tm_dy, dy, rows, n, ld_dy, true) ||
+    // (no map of no rows; the kernel then only reports a row count above 0 and reads nothing)
+    if (!encode_operand(&tm_dy, dy, rows > 0 ? rows : 1, n, ld_dy, true) ||
         !encode_output(&tm_dw, dw, n, d, ld_dw, true))
         return LEMO_ERR_CUDA;
     const auto kernel = checkpoint->format == LEMO_CHECKPOINT_E4M3 ? wg::wgrad_kernel<lemo::ckpt::kE4M3>

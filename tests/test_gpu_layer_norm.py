@@ -1,5 +1,7 @@
 """pipeline.Layer with norms on a GPU: sublayers that share one Layer."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -128,3 +130,27 @@ def test_backward_calls_on_two_streams(monkeypatch):
 
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(want, run(replay)))
+
+
+def test_no_room_for_any_row():
+    """Buffers of no rows: nothing is touched, and a kept total above zero is reported by every call
+    of the shared rule."""
+    lib = lemo.load()
+    d = 64
+    full, none = torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mem = torch.full((4, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.ones(d, d, device="cuda")
+    u8 = torch.zeros(4, d, dtype=torch.uint8, device="cuda")
+    c = lemo.lemo_checkpoint(0, d, u8.data_ptr(), d, u8.data_ptr(), 4, 0)
+    ck, m = ctypes.addressof(c), mem.data_ptr()
+    for total, status in ((full, lemo.LEMO_ERR_CAPACITY), (none, lemo.LEMO_OK)):
+        K = total.data_ptr()
+        calls = [lambda: lib.lemo_checkpoint_weight_grad(ck, m, d, 0, d, K, dw.data_ptr(), d, None),
+                 lambda: lib.lemo_checkpoint_restore(ck, K, 1, m, d, 0, None),
+                 lambda: lib.lemo_checkpoint_save(m, d, 4, None, K, ck, None),
+                 lambda: lib.lemo_gated_mlp(m, d, m, d, d, K, 1, m, d, 0, None, None, None),
+                 lambda: lib.lemo_norm_gather(RMS, m, d, 4, d, None, None, EPS, None, K, 1, m, d, 0, None, None,
+                                              None)]
+        for call in calls:
+            assert call() == lemo.LEMO_OK and lemo.lemo_get_error() == status
+    assert (mem == 3).all() and (dw == 1).all() and (u8 == 0).all()
