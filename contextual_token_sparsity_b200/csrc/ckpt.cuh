@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const RowsArgs a) {
     }
 }
 
-// A walk over items: 16384 x 4096 takes 35.6 us (89 % of the rate of a copy; 39.3
+// A walk over items: 16384 x 4096 takes 35.6 us (87 % of the rate of a copy; 39.3
 // with a warp per row, whose rounds of whole rows end unevenly).
 __global__ void __launch_bounds__(kThreads) restore_kernel(const RowsArgs a) {
     pdl_entry();

@@ -1251,7 +1251,8 @@ bool launch_norm(lemo::norm::Args& a, int dev, int sms, cudaStream_t st, int* gr
 // streams of 16 dvec bytes) and for the registers.  Measured at 8192 x 4096, us:
 // forward 256 x 2 x 2 32.8, 512 x 1 x 4 34.9, 512 x 1 x 2 40.9, 128 x 4 x 1 41.0;
 // backward with a mean and from codes 512 x 1 x 4 71.7, 256 x 2 x 2 92 (spills); at
-// 4096 x 8192 512 x 2 x 1 73.7, 512 x 2 x 2 92 (spills).
+// 4096 x 8192 512 x 2 x 1 73.7, 512 x 2 x 2 92 (spills); 512 x 1 x 4 takes 63 and 512 x 2 x 1 63
+// since the scale bytes are asked for with the copies.
 template <bool BWD, bool POST, bool FULL, bool CODED>
 lemo_status run_norm_as(lemo::norm::Args& a, cudaStream_t st, int* grid) {
     using lemo::norm::Shape;

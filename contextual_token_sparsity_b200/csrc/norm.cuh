@@ -29,11 +29,14 @@
 // second kernel in CTA order, so every result is deterministic.
 //
 // Measured on the copy rate's scale (6545 GB/s): gather of 8192 x 4096 RMS 27.6 us
-// (74 %), with an e4m3 checkpoint of the rows 35 us (73 %, issue slots 57 % busy), its
-// backward pass from bf16 rows 53 us (77 %) and from the checkpoint 53.6 us (67 %);
+// (74 %), with an e4m3 checkpoint of the rows 35 us (74 %, issue slots 57 % busy), its
+// backward pass from bf16 rows 53.7 us (76 %) and from the checkpoint 52.8 us (68 %);
+// layer norm with bias 31.3, 42.7, 55.4 and 63.2 us;
 // scatter of 16384 x 5120 RMS with a gate per token 103 us (99 %), its backward pass
 // 142 us (90 %).  Calls of less than 250 MB do not reach the copy rate: a plain copy
-// of 8192 x 4096 rows runs at 5.0 TB/s.
+// of 8192 x 4096 rows runs at 5.0 TB/s.  The backward passes with a mean spill registers
+// (17 warps: 96 each) and are furthest from it: scatter with a channel gate 52 us (59 %) at
+// 8192 x 4096, 100 (31 %) at 4096 x 8192 and 101 (30 %) at 2048 x 16384.
 #pragma once
 
 #include "ckpt.cuh"
@@ -227,8 +230,8 @@ constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 // How K rows are dealt.  Narrow rows (up to 1024 values): a CTA takes `m`
 // neighbouring rows per stage (as few as give every CTA the same number of stages),
 // and a slot keeps the rows of a stream together, so that rows that
-// are neighbours in memory come with one copy: 16384 x 512 is bound by the number
-// of copies, 18.4 us forward against 16.4.  Wide rows go round the CTAs one by one,
+// are neighbours in memory come with one copy: 16384 x 512 was bound by the number
+// of copies, 18.4 us forward with one per row, 15.2 so.  Wide rows go round the CTAs one by one,
 // each with its streams together: at 8192 x 5120 43 us forward so, 45 as above.
 template <typename S>
 struct Deal {

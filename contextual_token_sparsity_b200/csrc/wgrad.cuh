@@ -39,9 +39,11 @@
 // one before it has completed (a barrier in the next pair's CTA), so the order of
 // the adds stays fixed.  512 x 512 over 8192 rows: 25 us so, 50 without.
 //
-// Measured: 8192 rows, 4096 x 11008, e4m3: 591 us in a single launch (1.25 PFLOP/s,
-// tensor pipe 71 % busy), 678 us in a long loop, where the power limit lowers the
-// clock; 4928 rows, 4096 x 4096, int8: 145 and 169 us.
+// Measured: 8192 rows, 4096 x 11008, e4m3: 591 us in a single launch under the profiler
+// (1.25 PFLOP/s, tensor pipe 71 % busy), 664 to 683 us in long loops, where the power
+// limit lowers the clock; 4928 rows, 4096 x 4096, int8: 145 and 155 to 169 us.  Restoring
+// the rows to memory first and a library product take 579 us in loops of the first: what
+// this kernel saves is the copy, not time.
 //
 // Every wait is bounded in time; a wait that runs out records LEMO_ERR_TIMEOUT
 // and makes both CTAs of the pair drain what they issued, free their tensor

@@ -506,7 +506,8 @@ LEMO_API lemo_status lemo_segment_loss(const uint16_t* h, int64_t ld_h, int64_t 
  *  - kept_idx may be NULL: kept row r is then token r.
  *  - Calls that update token rows in place need kept_idx strictly ascending,
  *    as lemo_select writes it; an id that is out of range or not above the one
- *    before it is recorded as LEMO_ERR_INVALID_ARG and its row is skipped.
+ *    before it is recorded as LEMO_ERR_INVALID_ARG and its row is skipped
+ *    (a token whose rows are not neighbours, as in 5, 3, 5, ends undefined).
  *  - Zero tails: outputs that feed a GEMM over padded rows are written with
  *    zeros in rows [K, round_up(K, pad_to)); rows beyond are not touched.
  *  - Weight gradients are fp32 and ACCUMULATED (zero them for a fresh one);
@@ -565,7 +566,8 @@ typedef struct lemo_checkpoint {
  * checkpoint  optional: x[t] is also saved there as row r (checkpoint->d = d,
  *             checkpoint->rows >= rows).
  * One pass over x.  Ids may repeat or come in any order.  The squares are summed
- * in fp32: where that sum passes 3.4e38 the row's rstd is 0.
+ * in fp32: where that sum passes 3.4e38 the row's rstd is 0, and where every
+ * square is below 2^-150 and eps is 0 it is infinite.
  */
 LEMO_API lemo_status lemo_norm_gather(lemo_norm norm, const uint16_t* x, int64_t ld_x,
                                       int64_t x_rows, int32_t d, const uint16_t* weight,
